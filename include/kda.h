@@ -390,6 +390,138 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const v
                             const int32_t *num_tokens, int32_t update_state, void *o,
                             void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule (one decay per token and head)
+ *
+ * The scalar-decay relative of KDA, which the pages name as the special case of
+ * section 3.1 in which Diag(alpha) is one number per head ("Kimi K3:
+ * Architecture, Training, and Million-Token Agentic RL", section 3.1):
+ *     Sbar = e^{g_t} S_{t-1};  S_t = Sbar + beta_t k_t (v_t - Sbar^T k_t)^T;
+ *     o_t = scale S_t^T q_t
+ * Layouts as above, with these differences:
+ *     q, k    : [T, Hk, dk], Hk dividing H: value head h reads key head h / (H / Hk)
+ *     g, beta : [T, H] fp32; g <= 0 is the log-decay (values below -110, where
+ *               e^{g} is 0 in fp32, and -inf count as -110)
+ *
+ * States live in a pool `state` [pool_size, H, dk, dv] fp32 of fixed-size rows
+ * ("Kimi K3 Under the Hood", section "Serving two incompatible cache types":
+ * states kept at block boundaries next to the running ones, a prefix hit
+ * resuming from one).  A row index is read on the device; one outside
+ * [0, pool_size) means "no row": a source without a row is a zero state, a
+ * destination without one is not written.  Padding entries of a captured batch
+ * can therefore hold -1.  Several sequences may read one row (a shared prefix);
+ * a row that one sequence writes must not be read or written by another in the
+ * same call (a data race, not detected), but a sequence may write the row that
+ * it reads.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Bytes of device workspace kda_gdr_prefill needs for these sizes (an upper
+ * bound over every cu_seqlens with this total_tokens and num_seqs); 0 where none
+ * is needed and for invalid arguments.
+ */
+size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t Hk,
+                                      int32_t H, int32_t dk, int32_t dv, kda_dtype dt,
+                                      kda_algo algo);
+
+/*
+ * The gated delta rule over packed variable-length sequences.
+ *
+ *   cu_seqlens_dev, cu_seqlens_host, total_tokens, num_seqs  as kda_prefill.  The
+ *                   device offsets may end before total_tokens (a padded batch):
+ *                   rows of o behind the last sequence are left as they were.
+ *                   cu_seqlens_host, when given, must end at total_tokens; it
+ *                   only sets the order in which sequences start.
+ *   state, pool_size  the pool, or NULL with 0 (zero initial states, no final
+ *                   state; then src_slots, dst_slots and block_size must be
+ *                   absent too).
+ *   src_slots       device int32 [num_seqs]: the row each sequence starts from; NULL
+ *                   = zero states.
+ *   dst_slots       device int32 [num_seqs]: the row that receives the state after the
+ *                   sequence's last token; NULL = not written.  A sequence of
+ *                   length 0 passes its source state through.
+ *   ctx_lens        device int32 [num_seqs]: tokens each sequence had before this
+ *                   call (negative counts as 0), or NULL for 0.  Only
+ *                   the block boundaries depend on it.
+ *   block_table     device int32 [num_seqs, block_table_cols]: row j of sequence n
+ *                   is the pool row of its tokens j block_size .. (j + 1) block_size
+ *                   - 1.  With block_size > 0 (a positive multiple of 64) the state
+ *                   after every block that this call completes is written to that
+ *                   block's row; columns past block_table_cols have no row.
+ *                   block_size = 0: no such rows (block_table may be NULL).
+ *   workspace       at least kda_gdr_prefill_workspace_size bytes, 16-byte aligned
+ *                   (NULL when that is 0).
+ *   algo            KDA_ALGO_AUTO (tensor cores for bf16 with dk = dv = 128, else the
+ *                   fp32 recurrence on CUDA cores), KDA_ALGO_CUDA_CORE or
+ *                   KDA_ALGO_TENSOR_CORE (KDA_ERR_UNSUPPORTED for other types or
+ *                   sizes); KDA_ALGO_TENSOR_CORE_SPLIT is KDA_ERR_UNSUPPORTED.
+ */
+kda_status kda_gdr_prefill(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, const int32_t *cu_seqlens_dev,
+                           const int32_t *cu_seqlens_host, int32_t num_seqs,
+                           int32_t total_tokens, int32_t Hk, int32_t H, int32_t dk, int32_t dv,
+                           kda_dtype dt, float scale, float *state, int32_t pool_size,
+                           const int32_t *src_slots, const int32_t *dst_slots,
+                           const int32_t *ctx_lens, const int32_t *block_table,
+                           int32_t block_table_cols, int32_t block_size, void *o,
+                           void *workspace, size_t workspace_bytes, kda_algo algo, void *stream);
+
+/*
+ * The gated delta rule for Tq (1 .. 64) tokens of each of B sequences: decode
+ * (Tq = 1), speculative verify (update_state = 0: outputs only, the pool is left
+ * untouched) and replay (update_state = 1).
+ *
+ *   q, k [B, Tq, Hk, dk], v, o [B, Tq, H, dv]; g, beta [B, Tq, H] fp32.
+ *   src_slots    device int32 [B], or NULL for row b (then pool_size >= B).
+ *   dst_slots    device int32 [B], or NULL for the source row (in place); must be
+ *                NULL when update_state is 0.
+ *   num_tokens   device int32 [B]: tokens of sequence b to apply (clamped to
+ *                [0, Tq]), or NULL for all Tq.  Rows of o past it are left as
+ *                they were; a sequence with 0 passes its source state through.
+ *   o            may be NULL when update_state is 1.
+ */
+kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const float *g,
+                          const float *beta, int32_t B, int32_t Tq, int32_t Hk, int32_t H,
+                          int32_t dk, int32_t dv, kda_dtype dt, float scale, float *state,
+                          int32_t pool_size, const int32_t *src_slots, const int32_t *dst_slots,
+                          const int32_t *num_tokens, int32_t update_state, void *o, void *stream);
+
+/*
+ * Block tables and slot maps of a batch, built on the device from its request
+ * lengths ("Kimi K3 Under the Hood", section "Serving two incompatible cache
+ * types": one block table per request for states and for per-token caches).
+ * Request n has ctx_lens[n] tokens stored and gets new_lens[n] more (NULL
+ * ctx_lens = 0; negative lengths count as 0); block j of a request holds its
+ * tokens j block_size .. (j + 1) block_size - 1.
+ *
+ *   free_blocks     device int32 [num_free], free_head device int32 [1]: the blocks
+ *                   from entry free_head on are free (a negative head counts as 0).
+ *                   Requests take the blocks they newly reach from there, in
+ *                   request order.
+ *   block_table     device int32 [num_seqs, block_table_cols], in and out: entries of
+ *                   newly reached blocks are written, all others left as they
+ *                   were.  An entry that the free list cannot fill is -1;
+ *                   blocks past block_table_cols have no entry.
+ *   cu_seqlens      out [num_seqs + 1]: packed offsets of the new tokens.
+ *   positions       out [total_tokens] or NULL: position of each new token in its
+ *                   request.  total_tokens is the length of the two buffers; entries
+ *                   past the last new token are -1.
+ *   token_slots     out int64 [total_tokens] or NULL: block * block_size + offset in
+ *                   the block, -1 where there is no block.
+ *   src_slots, dst_slots  out [num_seqs] or NULL: the block of the request's last token
+ *                   before and after this call (-1 = none): the rows that
+ *                   kda_gdr_prefill, kda_gdr_decode read and write.
+ *   free_head_out   out [1]: free_head plus the blocks needed; a value above num_free
+ *                   says how many were missing.  May be free_head itself.
+ * Sums that pass 2^31 - 1 are written as 2^31 - 1.
+ */
+kda_status kda_block_plan(const int32_t *new_lens, const int32_t *ctx_lens, int32_t num_seqs,
+                          const int32_t *free_blocks, int32_t num_free, const int32_t *free_head,
+                          int32_t *block_table, int32_t block_table_cols, int32_t block_size,
+                          int32_t total_tokens, int32_t *cu_seqlens, int32_t *positions,
+                          int64_t *token_slots, int32_t *src_slots, int32_t *dst_slots,
+                          int32_t *free_head_out, void *stream);
+
 /*
  * Reads and clears the library's device status word for the current device
  * (synchronises `stream` first).  Kernels that wait on an on-chip barrier

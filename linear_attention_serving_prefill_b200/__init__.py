@@ -11,11 +11,13 @@ __all__ = ["kda_prefill", "kda_decode_step", "kda_prefill_workspace_size",
            "kda_status_string", "library_path", "KdaError", "kda_prefill_kernel_count",
            "kda_device_status", "kda_prefill_noalloc", "kda_prefill_checkpointed",
            "kda_checkpoint_count", "kda_decode_multi", "kda_prefill_segments",
-           "kda_prefill_debug", "kda_decode_check_slots"]
+           "kda_prefill_debug", "kda_decode_check_slots", "kda_gdr_prefill", "kda_gdr_decode",
+           "kda_gdr_prefill_workspace_size", "kda_block_plan", "BlockPlan"]
 
 
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)   # later accesses skip this hook
+        return value
     raise AttributeError(name)

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,7 +24,7 @@ STATUS_NAMES = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED",
                 3: "KDA_ERR_WORKSPACE", 4: "KDA_ERR_CUDA", 5: "KDA_ERR_TIMEOUT"}
 
 # Every exported symbol of include/kda.h, with its ctypes signature.
-_P, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_P, _I32, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "kda_abi_version": ([], _I32),
     "kda_status_string": ([_I32], ctypes.c_char_p),
@@ -46,6 +46,12 @@ SIGNATURES = {
     "kda_device_status": ([_P, _P], _I32),
     "kda_decode_multi": ([_P] * 6 + [_I32] * 6 + [_P, _I32, _P, _P, _I32, _P, _P], _I32),
     "kda_selftest_wait_timeout": ([ctypes.c_int64, _P], _I32),
+    "kda_gdr_prefill_workspace_size": ([_I32] * 8, _SZ),
+    "kda_gdr_prefill": ([_P] * 7 + [_I32] * 7 + [_F32, _P, _I32] + [_P] * 4 + [_I32] * 2
+                        + [_P] * 2 + [_SZ, _I32, _P], _I32),
+    "kda_gdr_decode": ([_P] * 5 + [_I32] * 7 + [_F32, _P, _I32] + [_P] * 3 + [_I32] + [_P] * 2,
+                       _I32),
+    "kda_block_plan": ([_P] * 2 + [_I32, _P, _I32, _P, _P] + [_I32] * 3 + [_P] * 7, _I32),
 }
 
 
@@ -344,3 +350,188 @@ def kda_decode_check_slots(slots_host, pool_size: int) -> bool:
     """True when the host slots are in range and distinct (kda_decode_check_slots)."""
     sl = torch.as_tensor(slots_host, dtype=torch.int32).contiguous()
     return _lib.kda_decode_check_slots(ctypes.c_void_p(sl.data_ptr()), sl.numel(), pool_size) == 0
+
+
+# ------------------------------------------------- gated delta rule, block plan --
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, device, shape=None):
+    """Address of a tensor that must be contiguous, of ``dtype`` and on ``device`` (and of
+    ``shape``); None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(fn, where: str, device, stream, *args):
+    """One library call on ``device``, on ``stream`` or that device's current stream."""
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, raw)
+    if code != 0:
+        raise KdaError(code, where)
+
+
+def _gdr_device(q, k, v):
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if q.dtype not in KDA_DTYPE:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    if k.shape != q.shape:
+        raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
+    if v.shape[:-2] != q.shape[:-2]:
+        raise ValueError("v must have q's leading dimensions")
+    return dev
+
+
+def _pool(state, H, dk, dv, device):
+    """Address and rows of the state pool [P, H, dk, dv]."""
+    if state is None:
+        return None, 0
+    return _ptr(state, "state", torch.float32, device, (state.shape[0], H, dk, dv)), state.shape[0]
+
+
+def kda_gdr_prefill_workspace_size(total_tokens: int, num_seqs: int, Hk: int, H: int, dk: int,
+                                   dv: int, dtype=torch.bfloat16, algo: str = "auto") -> int:
+    return int(_lib.kda_gdr_prefill_workspace_size(total_tokens, num_seqs, Hk, H, dk, dv,
+                                                   KDA_DTYPE[dtype], KDA_ALGO[algo]))
+
+
+def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=None,
+                    src_slots=None, dst_slots=None, ctx_lens=None, block_table=None,
+                    block_size: int = 0, scale: float = 1.0, o=None, workspace=None,
+                    algo: str = "auto", stream=None):
+    """Gated delta rule (one log-decay per token and head) over packed sequences; returns o.
+
+    q, k [T,Hk,dk], v [T,H,dv] (bf16 or fp32, one dtype), Hk dividing H; g, beta [T,H]
+    fp32; cu_seqlens [N+1] int32 on the device, cu_seqlens_host an optional CPU copy.
+    ``state`` [P,H,dk,dv] fp32 is a pool of state rows, updated in place: sequence n
+    starts from row src_slots[n] (None, or a row outside the pool: zeros) and leaves its
+    state in row dst_slots[n].  With ``block_size`` > 0 (a multiple of 64) the state after
+    every completed block of ctx_lens[n] + new tokens goes to its row of ``block_table``
+    [N, blocks].
+    """
+    dev = _gdr_device(q, k, v)
+    T, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    N = cu_seqlens.shape[0] - 1
+    dt = q.dtype
+    if o is None:
+        o = torch.empty_like(v)
+    need = _lib.kda_gdr_prefill_workspace_size(T, N, Hk, H, dk, dv, KDA_DTYPE[dt], KDA_ALGO[algo])
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    host = None
+    if cu_seqlens_host is not None:
+        if cu_seqlens_host.numel() != N + 1:
+            raise ValueError("cu_seqlens_host must have cu_seqlens' length")
+        ch = cu_seqlens_host.to(torch.int32).contiguous()
+        host = ch.data_ptr()
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr = _ptr(workspace, "workspace", workspace.dtype, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    pool, rows = _pool(state, H, dk, dv, dev)
+    cols = block_table.shape[1] if block_table is not None else 0
+    _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream,
+          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev),
+          _ptr(g, "g", torch.float32, dev, (T, H)), _ptr(beta, "beta", torch.float32, dev, (T, H)),
+          _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev), host, N, T, Hk, H, dk, dv,
+          KDA_DTYPE[dt], scale, pool, rows, _ptr(src_slots, "src_slots", torch.int32, dev, (N,)),
+          _ptr(dst_slots, "dst_slots", torch.int32, dev, (N,)),
+          _ptr(ctx_lens, "ctx_lens", torch.int32, dev, (N,)),
+          _ptr(block_table, "block_table", torch.int32, dev, (N, cols)), cols, block_size,
+          _ptr(o, "o", dt, dev, v.shape), ws_ptr, ws_bytes, KDA_ALGO[algo])
+    return o
+
+
+def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_tokens=None,
+                   update_state: bool = True, scale: float = 1.0, o=None,
+                   want_outputs: bool = True, stream=None):
+    """Gated delta rule for one or a few tokens of each sequence; returns o (or None).
+
+    q, k [B,Hk,dk] or [B,Tq,Hk,dk], v [B,(Tq,)H,dv], g, beta [B,(Tq,)H] fp32, Tq <= 64;
+    ``state`` [P,H,dk,dv] fp32 is the pool.  Sequence b reads row src_slots[b] (None: b)
+    and, with ``update_state``, writes row dst_slots[b] (None: the row it read) after its
+    first num_tokens[b] tokens; rows outside the pool are zeros / not written.
+    ``update_state=False`` is a verify pass.
+    """
+    dev = _gdr_device(q, k, v)
+    Tq = 1 if q.dim() == 3 else q.shape[1]
+    B, Hk, dk = q.shape[0], q.shape[-2], q.shape[-1]
+    H, dv = v.shape[-2:]
+    dt = q.dtype
+    if o is None and (want_outputs or not update_state):
+        o = torch.empty_like(v)
+    pool, rows = _pool(state, H, dk, dv, dev)
+    lead = v.shape[:-1]
+    _call(_lib.kda_gdr_decode, "kda_gdr_decode", dev, stream,
+          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev),
+          _ptr(g, "g", torch.float32, dev, lead), _ptr(beta, "beta", torch.float32, dev, lead),
+          B, Tq, Hk, H, dk, dv, KDA_DTYPE[dt], scale, pool, rows,
+          _ptr(src_slots, "src_slots", torch.int32, dev, (B,)),
+          _ptr(dst_slots, "dst_slots", torch.int32, dev, (B,)),
+          _ptr(num_tokens, "num_tokens", torch.int32, dev, (B,)), 1 if update_state else 0,
+          _ptr(o, "o", dt, dev, v.shape))
+    return o
+
+
+class BlockPlan(NamedTuple):
+    """What kda_block_plan writes (device tensors); the block table is updated in place."""
+    cu_seqlens: torch.Tensor    # [N+1] int32
+    positions: torch.Tensor     # [T] int32
+    token_slots: torch.Tensor   # [T] int64
+    src_slots: torch.Tensor     # [N] int32
+    dst_slots: torch.Tensor     # [N] int32
+    free_head: torch.Tensor     # [1] int32
+
+
+def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, block_size: int,
+                   total_tokens: int, out: Optional[BlockPlan] = None, stream=None) -> BlockPlan:
+    """Block tables and slot maps from request lengths, on the device.
+
+    new_lens [N] int32 (tokens of this call), ctx_lens [N] int32 or None (tokens stored
+    before it), free_blocks [F] int32 with free_head [1] int32 (entries from there on are
+    free), block_table [N,M] int32, extended in place.  ``total_tokens`` is the length of
+    the token outputs (entries past the last token are -1).  Returns a ``BlockPlan``;
+    ``out`` passes its tensors (``out.free_head`` may be ``free_head`` itself).
+    """
+    dev = new_lens.device
+    if dev.type != "cuda":
+        raise ValueError("new_lens must be a CUDA tensor")
+    N, F = new_lens.shape[0], free_blocks.shape[0]
+    i32 = torch.int32
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table must have shape ({N}, blocks)")
+    if total_tokens < 0:
+        raise ValueError("total_tokens must not be negative")
+    if out is None:
+        # One allocation: the int64 slots first, then every int32 output.
+        buf = torch.empty(12 * total_tokens + 4 * (3 * N + 2), dtype=torch.uint8, device=dev)
+        ints = buf[8 * total_tokens:].view(i32)
+        out = BlockPlan(ints[:N + 1], ints[3 * N + 2:], buf[:8 * total_tokens].view(torch.int64),
+                        ints[N + 1:2 * N + 1], ints[2 * N + 1:3 * N + 1],
+                        ints[3 * N + 1:3 * N + 2])
+    _call(_lib.kda_block_plan, "kda_block_plan", dev, stream,
+          _ptr(new_lens, "new_lens", i32, dev, (N,)), _ptr(ctx_lens, "ctx_lens", i32, dev, (N,)),
+          N, _ptr(free_blocks, "free_blocks", i32, dev, (F,)), F,
+          _ptr(free_head, "free_head", i32, dev, (1,)),
+          _ptr(block_table, "block_table", i32, dev), block_table.shape[1], block_size,
+          total_tokens, _ptr(out.cu_seqlens, "cu_seqlens", i32, dev, (N + 1,)),
+          _ptr(out.positions, "positions", i32, dev, (total_tokens,)),
+          _ptr(out.token_slots, "token_slots", torch.int64, dev, (total_tokens,)),
+          _ptr(out.src_slots, "src_slots", i32, dev, (N,)),
+          _ptr(out.dst_slots, "dst_slots", i32, dev, (N,)),
+          _ptr(out.free_head, "free_head", i32, dev, (1,)))
+    return out

@@ -1,0 +1,463 @@
+"""Gated delta rule on the GPU against the plain 64-bit form.
+
+Tolerances, relative to the largest reference magnitude of a tensor.  Storing an
+output in bf16 is off by at most 2^-8 of its value, so o of the fp32 recurrence gets
+2^-8 plus the fp32 allowance; that allowance, 1e-4, and the tensor-core bar, 2e-2 (a
+value passes at most five bf16 roundings, 5 * 2^-8 = 1.95e-2: T, W or U, the copy of
+S, delta, and the output), are the library's parity bars."""
+import pytest
+import torch
+
+from tests import gdr_testutil as U
+
+pytestmark = pytest.mark.gpu
+
+TOL_F32, TOL_TC = 1e-4, 2e-2
+TOL_O = {"f32": TOL_F32, "bf16": 2.0 ** -8 + TOL_F32}
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+ALGOS = ["cuda_core"]
+
+
+@pytest.fixture(scope="module")
+def K():
+    from linear_attention_serving_prefill_b200 import binding
+    return binding
+
+
+def i32(x):
+    return None if x is None else torch.as_tensor(x, dtype=torch.int32).cuda()
+
+
+def dev(x):
+    return {n: t.cuda() for n, t in x.items()}
+
+
+def algos_for(dtype, dk, dv):
+    return [a for a in ALGOS if a == "cuda_core" or (dtype == "bf16" and dk == 128 and dv == 128)]
+
+
+def run_prefill(K, x, lens, state, src, dst, algo, scale, ctx=None, table=None, block=0,
+                host=True, pad=0):
+    """Returns (o, pool); o starts as a pattern so that untouched rows show."""
+    cu = U.cu_of(lens)
+    d = dev(x)
+    o = torch.full(x["v"].shape, 7.0, dtype=x["v"].dtype, device="cuda")
+    st = None if state is None else state.cuda()
+    K.kda_gdr_prefill(d["q"], d["k"], d["v"], d["g"], d["beta"], cu.cuda(),
+                      cu if host and not pad else None, state=st, src_slots=i32(src),
+                      dst_slots=i32(dst), ctx_lens=i32(ctx),
+                      block_table=None if table is None else i32(table), block_size=block,
+                      scale=scale, o=o, algo=algo)
+    torch.cuda.synchronize()
+    assert K.kda_device_status() == 0
+    return o, st
+
+
+def spans_of(lens):
+    cu = U.cu_of(lens).tolist()
+    return [(cu[n], lens[n]) for n in range(len(lens))]
+
+
+def check_prefill(K, x, lens, H, state, src, dst, scale, dtype, algo, ctx=None, table=None,
+                  block=0, host=True, pad=0):
+    ref_o, ref_S = U.reference(x, spans_of(lens), H, scale, state, src, dst, ctx, table, block)
+    o, S = run_prefill(K, x, lens, state, src, dst, algo, scale, ctx, table, block, host, pad)
+    T = sum(lens)
+    tc = algo == "tensor_core"
+    assert U.max_err(o[:T], ref_o[:T]) <= (TOL_TC if tc else TOL_O[dtype])
+    if pad:
+        assert bool((o[T:] == 7.0).all())
+    if state is not None:
+        touched = set() if table is None else {r for row in table.tolist() for r in row}
+        touched |= set(dst or [])
+        for r in range(state.shape[0]):
+            if r in touched and not torch.equal(ref_S[r], state[r].double()):
+                assert U.max_err(S[r], ref_S[r]) <= (TOL_TC if tc else TOL_F32), f"row {r}"
+            else:
+                assert torch.equal(S[r].cpu(), state[r]), f"row {r} was written"
+    return o, S
+
+
+LENS = [[1], [2, 1, 3], [63], [64], [65], [16, 17, 0, 130, 1], [128, 129], [127, 0, 0, 64], [300]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("f32", 128, 128), ("f32", 64, 32),
+                                         ("bf16", 32, 128), ("f32", 32, 64), ("bf16", 64, 64)])
+def test_prefill_lengths(K, lens, dtype, dk, dv):
+    Hk, H = 2, 4
+    x = U.tokens((sum(lens),), Hk, H, dk, dv, DT[dtype], seed=len(lens))
+    N = len(lens)
+    state = U.pool(2 * N + 1, H, dk, dv, seed=3)
+    src = [i if i % 3 != 1 else -1 for i in range(N)]
+    dst = [N + i for i in range(N)]
+    for algo in algos_for(dtype, dk, dv):
+        check_prefill(K, x, lens, H, state, src, dst, dk ** -0.5, dtype, algo)
+
+
+@pytest.mark.parametrize("Hk,H", [(1, 1), (1, 3), (3, 3), (2, 10), (5, 5)])
+def test_prefill_head_groups(K, Hk, H):
+    lens = [70, 5]
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((75,), Hk, H, 128, 128, DT[dtype], seed=Hk)
+        state = U.pool(2, H, 128, 128, seed=5)
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, H, state, [0, 1], [0, 1], 1.0, dtype, algo, host=False)
+
+
+def test_prefill_without_pool(K):
+    lens = [40, 100]
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((140,), 2, 2, 128, 128, DT[dtype], seed=8)
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, 2, None, None, None, 0.5, dtype, algo)
+
+
+@pytest.mark.parametrize("ctx", [[0, 0, 0], [64, 5, 127], [1000, 1, 63], [128, 192, -3]], ids=str)
+@pytest.mark.parametrize("block", [64, 128])
+def test_prefill_block_rows(K, ctx, block):
+    """A block's row gets the state at its boundary of the absolute position."""
+    lens = [200, 130, 64]
+    N, H = 3, 2
+    pos = [max(c, 0) for c in ctx]
+    cols = max((c + n) // block for c, n in zip(pos, lens)) + 1
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((sum(lens),), 1, H, 128, 128, DT[dtype], seed=11)
+        state = U.pool(2 * N + N * cols, H, 128, 128, seed=12)
+        table = torch.arange(2 * N, 2 * N + N * cols, dtype=torch.int32).view(N, cols)
+        table[1, -2:] = -1                       # blocks without a row
+        table[2, 0] = state.shape[0] + 5         # a row outside the pool
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, H, state, [0, -1, 2], [3, 4, 5], 0.3, dtype, algo, ctx=pos,
+                          table=table, block=block)
+            if min(ctx) < 0:                     # a negative context counts as none
+                a = run_prefill(K, x, lens, state, [0, -1, 2], [3, 4, 5], algo, 0.3, ctx, table, block)
+                b = run_prefill(K, x, lens, state, [0, -1, 2], [3, 4, 5], algo, 0.3, pos, table, block)
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_prefill_fewer_table_columns_than_blocks(K):
+    lens = [300]
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((300,), 1, 1, 128, 128, DT[dtype], seed=13)
+        state = U.pool(4, 1, 128, 128, seed=14)
+        table = torch.tensor([[1, 2]], dtype=torch.int32)
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, 1, state, [0], [3], 1.0, dtype, algo, table=table, block=64)
+
+
+def test_prefill_rows_in_place_shared_and_missing(K):
+    """In-place rows, one row read by several sequences, rows outside the pool."""
+    lens = [70, 64, 3, 0, 0]
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((sum(lens),), 2, 2, 128, 128, DT[dtype], seed=15)
+        state = U.pool(6, 2, 128, 128, seed=16)
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, 2, state, [0, 1, 1, 1, 99], [0, 2, -7, 3, 4], 1.0, dtype, algo)
+
+
+@pytest.mark.parametrize("what", ["alpha1", "fast", "neg_inf", "beta0", "same_key", "mixed"])
+def test_prefill_decays(K, what):
+    """No decay, decays that wipe the state, g = -inf, beta = 0, one repeated key."""
+    lens = [150]
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((150,), 1, 3, 128, 128, DT[dtype], seed=17)
+        if what == "alpha1":
+            x["g"] = torch.zeros_like(x["g"])
+        elif what == "fast":
+            x["g"] = x["g"] * 100 - 20
+        elif what == "neg_inf":
+            x["g"][::7] = -float("inf")
+        elif what == "beta0":
+            x["beta"] = torch.zeros_like(x["beta"])
+        elif what == "same_key":
+            x["k"] = x["k"][:1].expand_as(x["k"]).contiguous()
+            x["beta"] = torch.ones_like(x["beta"])
+            x["g"] = x["g"] * 0.01
+        else:
+            x["g"][:, 0] = -200.0
+            x["g"][:, 1] = 0.0
+        state = U.pool(2, 3, 128, 128, seed=18, std=1.0)
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, 3, state, [0], [1], 1.0, dtype, algo)
+
+
+def test_prefill_padded_batch_and_foreign_values(K):
+    """Device offsets that end before the buffers do: rows behind stay as they were, and
+    infinities and NaN there, or in another sequence, reach no result."""
+    lens = [37, 90, 1]
+    T, pad = sum(lens), 50
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((T + pad,), 2, 2, 128, 128, DT[dtype], seed=19)
+        for n in ("q", "k", "v", "g", "beta"):
+            x[n][T:] = float("nan")
+            x[n][T + 3:T + 9] = float("inf")
+        state = U.pool(6, 2, 128, 128, seed=20)
+        for algo in algos_for(dtype, 128, 128):
+            check_prefill(K, x, lens, 2, state, [0, 1, 2], [3, 4, 5], 1.0, dtype, algo, pad=pad)
+        # A poisoned middle sequence: its neighbours are bit-equal to a clean run.
+        for algo in algos_for(dtype, 128, 128):
+            a, Sa = run_prefill(K, x, lens, state, [0, 1, 2], [3, 4, 5], algo, 1.0, pad=pad)
+            y = {n: t.clone() for n, t in x.items()}
+            for n in ("q", "k", "v"):
+                y[n][37:127] = float("nan")
+                y[n][40:50] = float("inf")
+            b, Sb = run_prefill(K, y, lens, state, [0, 1, 2], [3, 4, 5], algo, 1.0, pad=pad)
+            assert torch.equal(a[:37], b[:37]) and torch.equal(a[127:], b[127:])
+            assert torch.equal(Sa[3], Sb[3]) and torch.equal(Sa[5], Sb[5])
+            assert bool(torch.isnan(b[37:127]).any())
+
+
+def test_prefill_split_in_two_calls_continues(K):
+    """Two calls with the state carried in the pool equal one call (block rows too)."""
+    for dtype in ("f32", "bf16"):
+        x = U.tokens((333,), 1, 2, 128, 128, DT[dtype], seed=21)
+        state = U.pool(8, 2, 128, 128, seed=22)
+        table = torch.tensor([[3, 4, 5, 6]], dtype=torch.int32)
+        for algo in algos_for(dtype, 128, 128):
+            ref_o, ref_S = U.reference(x, [(0, 333)], 2, 1.0, state, [0], [1], None, table, 64)
+            tol = (TOL_TC, TOL_TC) if algo == "tensor_core" else (TOL_O[dtype], TOL_F32)
+            for cut in (1, 64, 100, 320):
+                first = {n: t[:cut].contiguous() for n, t in x.items()}
+                rest = {n: t[cut:].contiguous() for n, t in x.items()}
+                oa, S = run_prefill(K, first, [cut], state, [0], [2], algo, 1.0, [0], table, 64)
+                ob, S = run_prefill(K, rest, [333 - cut], S.cpu(), [2], [1], algo, 1.0, [cut], table, 64)
+                assert U.max_err(torch.cat([oa, ob]), ref_o) <= tol[0]
+                for r in (1, 3, 4, 5, 6):
+                    assert U.max_err(S[r], ref_S[r]) <= tol[1], (cut, r)
+
+
+@pytest.mark.parametrize("Tq", [1, 2, 3, 8, 9, 64])
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("f32", 128, 64), ("f32", 32, 32),
+                                         ("bf16", 64, 128)])
+def test_decode(K, Tq, dtype, dk, dv):
+    B, Hk, H = 5, 2, 6
+    x = U.tokens((B * Tq,), Hk, H, dk, dv, DT[dtype], seed=Tq)
+    state = U.pool(12, H, dk, dv, seed=23)
+    nt = [Tq, 0, (Tq + 1) // 2, Tq + 3, -2]
+    applied = [min(max(n, 0), Tq) for n in nt]
+    src, dst = [3, 0, -1, 7, 2], [8, 1, 9, 7, 40]
+    d = {n: t.cuda().view(B, Tq, *t.shape[1:]) for n, t in x.items()}
+    spans = [(b * Tq, applied[b]) for b in range(B)]
+    ref_o, ref_S = U.reference(x, spans, H, 0.7, state, src, dst)
+    live = torch.isfinite(ref_o)
+    ref_o = torch.where(live, ref_o, torch.full_like(ref_o, 7.0))
+    for update in (True, False):
+        st = state.cuda()
+        o = torch.full_like(d["v"], 7.0)
+        K.kda_gdr_decode(d["q"], d["k"], d["v"], d["g"], d["beta"], st, src_slots=i32(src),
+                         dst_slots=i32(dst) if update else None, num_tokens=i32(nt),
+                         update_state=update, scale=0.7, o=o)
+        flat = o.view(B * Tq, H, dv).cpu()
+        assert bool((flat[~live] == 7.0).all())
+        assert U.max_err(flat, ref_o) <= TOL_O[dtype]
+        if update:
+            for r in range(12):
+                if r in dst:
+                    assert U.max_err(st[r], ref_S[r]) <= TOL_F32
+                else:
+                    assert torch.equal(st[r].cpu(), state[r])
+        else:
+            assert torch.equal(st.cpu(), state)
+
+
+def test_decode_defaults(K):
+    """No slots: row b in place; three-dimensional tokens; no outputs wanted."""
+    B, H = 4, 2
+    x = U.tokens((B,), 1, H, 128, 128, torch.bfloat16, seed=30)
+    state = U.pool(B + 1, H, 128, 128, seed=31)
+    d = dev(x)
+    st = state.cuda()
+    o = K.kda_gdr_decode(d["q"], d["k"], d["v"], d["g"], d["beta"], st)
+    rows = list(range(B))
+    ref_o, ref_S = U.reference(x, [(b, 1) for b in rows], H, 1.0, state, rows, rows)
+    assert U.max_err(o, ref_o) <= TOL_O["bf16"] and U.max_err(st, ref_S) <= TOL_F32
+    again = state.cuda()
+    assert K.kda_gdr_decode(d["q"], d["k"], d["v"], d["g"], d["beta"], again, want_outputs=False) is None
+    assert torch.equal(st, again)
+
+
+def test_decode_far_rows(K):
+    """Pool rows whose element offsets pass 32 bits."""
+    H, P = 96, 1500
+    state = torch.zeros(P, H, 128, 128, device="cuda")
+    x = U.tokens((2,), 1, H, 128, 128, torch.bfloat16, seed=32)
+    row = U.pool(1, H, 128, 128, seed=33)
+    state[P - 1].copy_(row[0])
+    d = dev(x)
+    o = K.kda_gdr_decode(d["q"], d["k"], d["v"], d["g"], d["beta"], state,
+                         src_slots=i32([P - 1, 0]), dst_slots=i32([P - 2, 1]))
+    big = torch.cat([row, torch.zeros(3, H, 128, 128)])
+    ref_o, ref_S = U.reference(x, [(0, 1), (1, 1)], H, 1.0, big, [0, 1], [2, 3])
+    assert U.max_err(o, ref_o) <= TOL_O["bf16"]
+    assert U.max_err(state[P - 2], ref_S[2]) <= TOL_F32
+    assert U.max_err(state[1], ref_S[3]) <= TOL_F32
+    for algo in algos_for("bf16", 128, 128):
+        cu = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+        K.kda_gdr_prefill(d["q"], d["k"], d["v"], d["g"], d["beta"], cu, state=state,
+                          src_slots=i32([P - 1]), dst_slots=i32([P - 3]), algo=algo)
+        _, S = U.reference(x, [(0, 2)], H, 1.0, big, [0], [2])
+        assert U.max_err(state[P - 3], S[2]) <= (TOL_TC if algo == "tensor_core" else TOL_F32)
+    del state
+
+
+def plan_tensors(new, ctx, free, head, table):
+    return (i32(new), i32(ctx), i32(free), i32([head]), i32(table))
+
+
+@pytest.mark.parametrize("case", [
+    dict(new=[1, 1, 1], ctx=[0, 5, 64], bs=64, F=20),
+    dict(new=[0, 7, 0, 200, 1], ctx=[0, 0, 3, 60, 127], bs=16, F=40),
+    dict(new=[5, 5, 5], ctx=None, bs=4, F=4),                    # the free list runs out
+    dict(new=[100, 30], ctx=[0, 50], bs=16, F=40, cols=4),       # blocks past the table
+    dict(new=[-3, 4], ctx=[2, -9], bs=3, F=9),                   # negative lengths count as 0
+    dict(new=[9], ctx=[7], bs=1, F=30),
+], ids=str)
+@pytest.mark.parametrize("head,extra", [(0, 0), (2, 5), (-4, 0)])
+def test_plan(K, case, head, extra):
+    new, ctx, bs = case["new"], case["ctx"], case["bs"]
+    c = [0] * len(new) if ctx is None else ctx
+    cols = case.get("cols") or max(-(-(max(a, 0) + max(b, 0)) // bs) for a, b in zip(c, new)) + 1
+    free = torch.randperm(case["F"], generator=torch.Generator().manual_seed(1)).tolist()
+    table = [[1000 + 10 * n + j if j < -(-max(c[n], 0) // bs) else -7 for j in range(cols)]
+             for n in range(len(new))]
+    T = sum(max(x, 0) for x in new) + extra
+    ref = U.plan_reference(new, ctx, free, head, table, bs, T)
+    t = plan_tensors(new, ctx, free, head, table)
+    p = K.kda_block_plan(t[0], t[1], t[2], t[3], t[4], bs, T)
+    got = [p.cu_seqlens, p.positions, p.token_slots, p.src_slots, p.dst_slots, p.free_head, t[4]]
+    for g, r in zip(got, [*ref[:5], [ref[5]], ref[6]]):
+        assert g.tolist() == r
+
+
+@pytest.mark.parametrize("N,hi,bs,seed", [(1, 9000, 64, 0), (1024, 9, 16, 1), (1025, 40, 64, 2),
+                                          (3000, 3, 512, 3), (70, 500, 16, 4), (5, 20000, 128, 5)])
+def test_plan_large(K, N, hi, bs, seed):
+    gen = torch.Generator().manual_seed(seed)
+    new = torch.randint(0, hi + 1, (N,), generator=gen).tolist()
+    ctx = torch.randint(0, 300, (N,), generator=gen).tolist()
+    cols = max(-(-(a + b) // bs) for a, b in zip(ctx, new)) + 1
+    need = sum(-(-(a + b) // bs) - -(-a // bs) for a, b in zip(ctx, new))
+    free = torch.randperm(need + 5, generator=gen).tolist()
+    table = torch.randint(0, 1000, (N, cols), generator=gen).tolist()
+    T = sum(new)
+    ref = U.plan_reference(new, ctx, free, 3, table, bs, T)
+    t = plan_tensors(new, ctx, free, 3, table)
+    p = K.kda_block_plan(t[0], t[1], t[2], t[3], t[4], bs, T)
+    got = [p.cu_seqlens, p.positions, p.token_slots, p.src_slots, p.dst_slots, p.free_head, t[4]]
+    for g, r in zip(got, [*ref[:5], [ref[5]], ref[6]]):
+        assert g.tolist() == r
+
+
+def test_plan_fewer_token_entries_than_tokens(K):
+    """A token buffer shorter than the batch is filled to its end, no further."""
+    t = plan_tensors([10, 10], [0, 0], list(range(8)), 0, [[-1] * 4] * 2)
+    p = K.kda_block_plan(*t, 4, 13)
+    ref = U.plan_reference([10, 10], [0, 0], list(range(8)), 0, [[-1] * 4] * 2, 4, 20)
+    assert p.positions.tolist() == ref[1][:13] and p.token_slots.tolist() == ref[2][:13]
+    assert p.cu_seqlens.tolist() == [0, 10, 20]
+
+
+def serve(K, x, prompt, steps, H, block, algo, rows, graph=False):
+    """Plan -> prefill -> (plan -> decode) x steps over one pool; returns the outputs per
+    request and the pool with its table."""
+    N = len(prompt)
+    total = [p + steps for p in prompt]
+    d = dev(x)
+    start = U.cu_of(total).tolist()
+    idx = torch.cat([torch.arange(start[n], start[n] + prompt[n]) for n in range(N)]).cuda()
+    cols = max(-(-t // block) for t in total)
+    table = torch.full((N, cols), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(rows, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()
+    head = i32([0])
+    pool = torch.full((rows, H, 128, 128), float("nan"), device="cuda")
+    new, ctx = i32(prompt), i32([0] * N)
+    p = K.kda_block_plan(new, ctx, free, head, table, block, sum(prompt))
+    sel = {n: t[idx].contiguous() for n, t in d.items()}
+    o = torch.zeros_like(d["v"])
+    o[idx] = K.kda_gdr_prefill(sel["q"], sel["k"], sel["v"], sel["g"], sel["beta"], p.cu_seqlens,
+                               state=pool, src_slots=p.src_slots, dst_slots=p.dst_slots,
+                               ctx_lens=ctx, block_table=table, block_size=block, scale=0.5,
+                               algo=algo)
+    head.copy_(p.free_head)
+    one = i32([1] * N)
+    ctx.copy_(new)
+    at = torch.tensor(start[:N]).cuda() + ctx
+    tok = {n: t[at].contiguous() for n, t in d.items()}
+    out = torch.empty_like(tok["v"])
+    pl = K.kda_block_plan(one, ctx, free, head, table.clone(), block, N)   # its buffers
+    plan = K.BlockPlan(pl.cu_seqlens, pl.positions, pl.token_slots, pl.src_slots, pl.dst_slots, head)
+
+    def decode():
+        K.kda_block_plan(one, ctx, free, head, table, block, N, out=plan)
+        K.kda_gdr_decode(tok["q"], tok["k"], tok["v"], tok["g"], tok["beta"], pool,
+                         src_slots=plan.src_slots, dst_slots=plan.dst_slots, scale=0.5, o=out)
+        ctx.add_(one)
+
+    run = decode
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            decode()
+        run = g.replay
+    for _ in range(steps):
+        for n, t in d.items():
+            tok[n].copy_(t[at])
+        run()
+        o[at] = out
+        at += 1
+    torch.cuda.synchronize()
+    return o, pool, table, int(head)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_serving_run(K, graph):
+    """A run of them together: every output, every completed block's row and the last
+    rows equal the plain form, eagerly and with the step captured in a graph."""
+    prompt, steps, H, block = [60, 128, 1, 190], 70, 2, 64
+    total = [p + steps for p in prompt]
+    x = U.tokens((sum(total),), 1, H, 128, 128, torch.bfloat16, seed=40)
+    need = sum(-(-t // block) for t in total)
+    ids = torch.arange(need, dtype=torch.int32)
+    cols = max(-(-t // block) for t in total)
+    ref_table = torch.full((4, cols), -1, dtype=torch.int32)
+    at = 0
+    for n, t in enumerate(total):
+        ref_table[n, :-(-t // block)] = ids[at:at - (-t // block)]
+        at += -(-t // block)
+    dst = [int(ref_table[n, (t - 1) // block]) for n, t in enumerate(total)]
+    ref_o, ref_S = U.reference(x, spans_of(total), H, 0.5, torch.zeros(need, H, 128, 128), None,
+                               dst, None, ref_table, block)
+    for algo in algos_for("bf16", 128, 128):
+        o, pool, table, head = serve(K, x, prompt, steps, H, block, algo, need + 3, graph)
+        assert head == need
+        tol = (TOL_TC, TOL_TC) if algo == "tensor_core" else (TOL_O["bf16"], TOL_F32)
+        assert U.max_err(o, ref_o) <= tol[0]
+        for n, t in enumerate(total):
+            for j in range(-(-t // block)):
+                assert U.max_err(pool[int(table[n, j])], ref_S[int(ref_table[n, j])]) <= tol[1]
+        used = table[table >= 0].tolist()
+        assert len(set(used)) == need
+        rest = [r for r in range(need + 3) if r not in used]
+        assert bool(torch.isnan(pool[rest]).all())
+
+
+def test_streams_and_repeats(K):
+    """Two calls at once on two streams, and repeated calls, give the same bits."""
+    lens = [100, 260, 64]
+    x = U.tokens((sum(lens),), 2, 4, 128, 128, torch.bfloat16, seed=50)
+    state = U.pool(6, 4, 128, 128, seed=51)
+    for algo in algos_for("bf16", 128, 128):
+        o0, S0 = run_prefill(K, x, lens, state, [0, 1, 2], [3, 4, 5], algo, 1.0)
+        d, cu = dev(x), U.cu_of(lens).cuda()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        outs, pools = [torch.empty_like(d["v"]) for _ in streams], [state.cuda() for _ in streams]
+        src, dst = i32([0, 1, 2]), i32([3, 4, 5])
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, o, st in zip(streams, outs, pools):
+                K.kda_gdr_prefill(d["q"], d["k"], d["v"], d["g"], d["beta"], cu, state=st,
+                                  src_slots=src, dst_slots=dst, o=o, algo=algo, stream=s)
+        torch.cuda.synchronize()
+        for o, st in zip(outs, pools):
+            assert torch.equal(o, o0) and torch.equal(st, S0)
