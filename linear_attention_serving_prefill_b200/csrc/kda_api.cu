@@ -112,6 +112,8 @@ int32_t segments_for(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t 
 
 }  // namespace
 
+bool kda::device_status_word(int32_t **out) { return status_word(out) == KDA_OK; }
+
 extern "C" int32_t kda_abi_version(void) { return KDA_ABI_VERSION; }
 
 extern "C" const char *kda_status_string(kda_status s)

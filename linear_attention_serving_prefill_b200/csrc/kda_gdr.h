@@ -41,6 +41,9 @@ cudaError_t launch_gdr_recurrent(const GdrArgs &a, cudaStream_t stream);
 // One token per sequence (a.Tq == 1), one pass over each state.
 cudaError_t launch_gdr_step(const GdrArgs &a, cudaStream_t stream);
 
+// Chunked prefill on tensor cores (bf16, dk = dv = 128; a.cu and a.status set).
+cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream);
+
 struct BlockPlanArgs {
     const int32_t *new_lens, *ctx_lens;
     int32_t num_seqs;

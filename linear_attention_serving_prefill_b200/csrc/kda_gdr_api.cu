@@ -32,8 +32,14 @@ kda_status check_prefill(int32_t total_tokens, int32_t num_seqs, int32_t Hk, int
     const kda_status st = check_sizes(Hk, H, dk, dv, dt);
     if (st != KDA_OK) return st;
     if (algo == KDA_ALGO_TENSOR_CORE_SPLIT) return KDA_ERR_UNSUPPORTED;
-    if (algo == KDA_ALGO_TENSOR_CORE) return KDA_ERR_UNSUPPORTED;
+    if (algo == KDA_ALGO_TENSOR_CORE && (dt != KDA_DTYPE_BF16 || dk != 128 || dv != 128))
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
+}
+
+bool use_tensor_core(int32_t dk, int32_t dv, kda_dtype dt, kda_algo algo)
+{
+    return algo != KDA_ALGO_CUDA_CORE && dt == KDA_DTYPE_BF16 && dk == 128 && dv == 128;
 }
 
 kda_status status_of(cudaError_t err) { return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
@@ -94,7 +100,10 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
     a.table = block_size > 0 ? block_table : nullptr;
     a.table_cols = block_table_cols; a.block = block_size;
     a.update = true;
-    return status_of(kda::launch_gdr_recurrent(a, (cudaStream_t)stream));
+    if (!use_tensor_core(dk, dv, dt, algo))
+        return status_of(kda::launch_gdr_recurrent(a, (cudaStream_t)stream));
+    if (!kda::device_status_word(&a.status)) return KDA_ERR_CUDA;
+    return status_of(kda::launch_gdr_tensor_core(a, (cudaStream_t)stream));
 }
 
 extern "C" kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const float *g,

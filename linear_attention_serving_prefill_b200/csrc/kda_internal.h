@@ -13,6 +13,10 @@ namespace kda {
 // cudaDeviceReset, gets a new one).  False when no context is current.
 bool current_context_id(unsigned long long *id);
 
+// Device address of the library's status word on the current device; false when
+// a CUDA call failed.
+bool device_status_word(int32_t **out);
+
 struct PrefillArgs {
     const void *q, *k, *v, *z;
     const float *A, *beta;

@@ -1,6 +1,7 @@
 // Tensor-core prefill path (tcgen05, bf16 operands, dk = dv = 128).
 #pragma once
 
+#include <cuda.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -25,6 +26,14 @@ int tc_split_segments(int32_t total_tokens, int32_t num_seqs, int32_t H, bool fo
 // diagonal tiles, 8 KiB per (chunk, head).
 size_t tc_workspace_bytes(int32_t total_tokens, int32_t num_seqs, int32_t H, int segments,
                           int gate = 0);
+
+// Tensor map of [T][H][128] bf16 rows with a {64 channels, 1 head, 64 tokens} box
+// and the 128-byte swizzle; false when the driver refuses it.
+bool tc_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H);
+
+// Tensor map of [T][H][128] bf16 output rows with a dense {channels, 1 head, 64
+// tokens} box.
+bool tc_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t channels);
 
 // Launches plan, intra-chunk and state kernels on `stream`, then, when
 // a.segments > 1, the segment composition and the output correction.

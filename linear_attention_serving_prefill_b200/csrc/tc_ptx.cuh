@@ -321,6 +321,18 @@ __device__ __forceinline__ uint64_t desc_kmajor_none(uint32_t saddr, uint32_t lb
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1u << 46);
 }
 
+// Shared-memory matrix descriptor for an MN-major operand in the 128-byte
+// swizzled layout: rows run along K, 64 M/N elements (128 B) each, groups of 8
+// rows 1024 B apart (stride offset), the next 64 M/N elements `lbo` bytes away
+// (leading offset).  A K = 16 step advances the start address by 2048 B.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// Bits of the instruction descriptor that mark A / B as MN-major.
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
+
 // Instruction descriptor, kind::f16 with bf16 A and B (both K-major) and an
 // fp32 accumulator: D format [4,6) = 1, A format [7,10) = 1, B format
 // [10,13) = 1, N >> 3 at [17,23), M >> 4 at [24,29).

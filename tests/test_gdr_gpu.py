@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 TOL_F32, TOL_TC = 1e-4, 2e-2
 TOL_O = {"f32": TOL_F32, "bf16": 2.0 ** -8 + TOL_F32}
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
-ALGOS = ["cuda_core"]
+ALGOS = ["cuda_core", "tensor_core"]
 
 
 @pytest.fixture(scope="module")
