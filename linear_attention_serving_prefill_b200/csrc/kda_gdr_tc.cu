@@ -12,19 +12,19 @@
 // factors e^{G_r - G_s}, r >= s, are formed without a reciprocal and are at most
 // 1 for g <= 0.
 //
-// One CTA of 18 warps owns a (sequence, value head) and walks its chunks with the
+// One CTA of 23 warps owns a (sequence, value head) and walks its chunks with the
 // fp32 state transposed in tensor memory.  Nothing goes through HBM but q, k, v,
 // g, beta, o and the state rows.  Roles:
 //   chain (warps 0-7)    E^T from its accumulator to bf16 operands (E for the
 //                        outputs, e^{G_C - G} E for the state); S^T to its bf16
 //                        copy, then the fp32 master times the next e^{G_C};
-//   intra (warps 8-11)   A and P from the accumulator with their decays, T by
-//                        16 x 16 forward substitution and two block doublings
-//                        (tf32 mma), T's two bf16 operands; runs a chunk ahead;
-//   aux   (warps 12-15)  Q <- e^G Q in place, W^T from its accumulator to a bf16
+//   intra (warps 8-15)   two groups, even and odd chunks: A and P from the accumulator
+//                        with their decays, T by 16 x 16 forward substitution and two
+//                        block doublings (tf32 mma), T's two bf16 operands;
+//   aux   (warps 16-19)  Q <- e^G Q in place, W^T from its accumulator to a bf16
 //                        operand, O^T to o;
-//   issue (warp 16)      the products of the state chain;
-//   load  (warp 17)      TMA tiles, and the decay tables of a chunk (a warp scan).
+//   issue (warps 20, 21) the products of the state chain; A, P and W's products;
+//   load  (warp 22)      TMA tiles, and the decay tables of a chunk (a warp scan).
 // Products (TMEM accumulators in brackets), chunk c:
 //   [AP] = [K; Q] K^T;  [W^T] = K^T (-T Diag(beta e^G))^T;  [E^T] = V^T (T Diag(beta))^T
 //   [E^T] += S^T (-W)^T;  [O^T] = S^T (e^G Q)^T
@@ -48,8 +48,8 @@ constexpr int kD = 128, kC = 64;              // head size, chunk
 constexpr uint64_t kWaitNs = 2000000000ull;   // per-wait limit: 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kChainThreads = 256, kIntraThreads = 128, kAuxThreads = 128;
-constexpr int kIntraWarp = 8, kAuxWarp = 12, kIssueWarp = 16, kLoadWarp = 17;
+constexpr int kChainThreads = 256, kGroupThreads = 128, kAuxThreads = 128;
+constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kIssue2Warp = 21, kLoadWarp = 22;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 
 // Shared memory (offsets from a 1024-aligned base).  A K/Q stage is
@@ -62,11 +62,12 @@ constexpr uint32_t kOffW = kOffV + kVStages * kVStage;   // W^T: 128 channels x 
 constexpr uint32_t kOffP = kOffW + 16384;                // P: 64 x 64, two buffers
 constexpr uint32_t kOffT1 = kOffP + 2 * 8192;            // -T Diag(beta e^G): 64 x 64
 constexpr uint32_t kOffT2 = kOffT1 + 8192;               // T Diag(beta)
-constexpr uint32_t kOffA = kOffT2 + 8192;                // A, then T: fp32 [64][68]
-constexpr int kLd = 68;
-constexpr uint32_t kOffO = kOffA + 64 * kLd * 4;         // output staging, 4 KiB a warp
+constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group: fp32 blocks, see kMBlock
+// A's 32 x 32 diagonal blocks (then T's) and its lower-left block, rows padded to 36.
+constexpr int kLd = 36, kMBlock = 32 * kLd;
+constexpr uint32_t kMGroup = 3 * kMBlock * 4;
+constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 4 KiB a warp
 constexpr uint32_t kSmem = kOffO + 4 * 4096 + 1024;
-static_assert(kOffO % 1024 == 0 && kOffA % 1024 == 0, "operand alignment");
 
 // TMEM columns.
 constexpr uint32_t kTS = 0;      // S^T, fp32 [dv][dk]
@@ -81,8 +82,8 @@ constexpr uint32_t kTW = 448;    // W^T accumulator [dk][token]
 struct Bars {
     uint64_t kq_full[kKQStages], kq_empty[kKQStages], gate_full[kKQStages];
     uint64_t v_full[kVStages], v_empty[kVStages];   // v_empty: E^T = V^T T.. done (T too)
-    uint64_t ap_full[2], o_full[2];
-    uint64_t t_ready, w_full, w_tfree, w_ready;
+    uint64_t ap_full[2], o_full[2], w_full[2], prep[2];
+    uint64_t ap_tfree, t_ready, w_tfree, w_ready;
     uint64_t s_ready, e_ready, decayed, e_full, s_full, o_free;
     uint64_t drain[2];
 };
@@ -95,7 +96,9 @@ struct __align__(16) Gate {
     float beta[kC];
     float nbe[kC];    // -beta 2^G
     float tail[kC];   // 2^(G_C - G)
-    float eGC, pad[3];
+    float eGC;        // 2^G_C
+    int steep;        // some tile decays by more than 2^-100: no factored form there
+    int pad[2];
 };
 
 struct Params {
@@ -130,13 +133,12 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void intra_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// The same barrier; true when any thread passed true.
-__device__ __forceinline__ bool intra_sync_any(bool pred) {
+// Barrier over one intra group; true when any of its threads passed true.
+__device__ __forceinline__ bool group_sync_any(int group, bool pred) {
     uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, 1, 128, p;\n"
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, %2, 128, p;\n"
                  " selp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r) : "r"((uint32_t)pred) : "memory");
+                 : "=r"(r) : "r"((uint32_t)pred), "r"(1 + group) : "memory");
     return r != 0;
 }
 __device__ __forceinline__ void tma_tile(void *smem_dst, const CUtensorMap *map, int x, int h, int t0,
@@ -157,13 +159,12 @@ __device__ __forceinline__ void named_timeout(int32_t *status) {
     atomicCAS(status, 0, (int32_t)KDA_TC_TIMEOUT_CODE);
 }
 
-// Block (bi, bj) of the lower-triangular inverse, of `W` = 16 or 32 columns, after both
-// diagonal neighbours are inverted in place: Z = -(T_ii A_ij) T_jj.  Y = T_ii A_ij for the
-// 16 rows r0.. of this warp; then NT 8-column tiles of Z from column n0 of the block.
-// All reads end before the caller's barrier; the caller stores z after it.
+// Off-diagonal block of the inverse of a lower-triangular matrix from its inverted diagonal
+// blocks: Z = (T_ii A_ij) T_jj (the caller negates), all blocks W x W with leading dimension
+// kLd.  This warp forms the 16 rows from rr, of them NT 8-column tiles from column n0.
 template <int W, int NT>
-__device__ __forceinline__ void block_product(const float *M, int i0, int j0, int rr, int n0, int lane,
-                                              float (&z)[NT][4]) {
+__device__ __forceinline__ void block_product(const float *Ti, const float *A, const float *Tj, int rr, int n0,
+                                              int lane, float (&z)[NT][4]) {
     const int g = lane >> 2, t = lane & 3;
     float y[W / 8][4];
 #pragma unroll
@@ -172,9 +173,9 @@ __device__ __forceinline__ void block_product(const float *M, int i0, int j0, in
     for (int k = 0; k < W; k += 8) {
         if (k >= rr + 16) break;    // T_ii is lower triangular
         uint32_t a[4];
-        const float *p = M + (i0 + rr + g) * kLd + i0 + k + t;
+        const float *p = Ti + (rr + g) * kLd + k + t;
         a[0] = tf32(p[0]); a[1] = tf32(p[8 * kLd]); a[2] = tf32(p[4]); a[3] = tf32(p[8 * kLd + 4]);
-        const float *q = M + (i0 + k + t) * kLd + j0 + g;
+        const float *q = A + (k + t) * kLd + g;
 #pragma unroll
         for (int n = 0; n < W / 8; ++n) mma_tf32(y[n], a, tf32(q[8 * n]), tf32(q[4 * kLd + 8 * n]));
     }
@@ -185,7 +186,7 @@ __device__ __forceinline__ void block_product(const float *M, int i0, int j0, in
 #pragma unroll
     for (int k = 0; k < W / 8; ++k) {
         const uint32_t a[4] = {tf32(y[k][0]), tf32(y[k][2]), tf32(y[k][1]), tf32(y[k][3])};
-        const float *q = M + (j0 + 8 * k + 2 * t) * kLd + j0 + n0 + g;
+        const float *q = Tj + (8 * k + 2 * t) * kLd + n0 + g;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             if (8 * k + 7 >= n0 + 8 * n) mma_tf32(z[n], a, tf32(q[8 * n]), tf32(q[kLd + 8 * n]));
@@ -241,10 +242,12 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&bars.v_empty[s], 1);
             mbar_init(&bars.ap_full[s], 1);
             mbar_init(&bars.o_full[s], 1);
+            mbar_init(&bars.w_full[s], 1);
+            mbar_init(&bars.prep[s], kGroupThreads);
             mbar_init(&bars.drain[s], 1);
         }
-        mbar_init(&bars.t_ready, 1);
-        mbar_init(&bars.w_full, 1);
+        mbar_init(&bars.ap_tfree, kGroupThreads);
+        mbar_init(&bars.t_ready, kGroupThreads);
         mbar_init(&bars.w_tfree, kAuxThreads);
         mbar_init(&bars.w_ready, kAuxThreads);
         mbar_init(&bars.s_ready, kChainThreads);
@@ -255,6 +258,12 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(&bars.o_free, kAuxThreads);
         fence_mbar_init();
     }
+    // The upper right quadrants of P and T's operands are zero in every chunk.
+    for (int e = tid; e < 4 * 32 * 4; e += kThreads) {
+        const uint32_t img = e < 256 ? kOffP + (e >> 7) * 8192 : (e < 384 ? kOffT1 : kOffT2);
+        *(uint4 *)(sm + img + sw128_offset((e >> 2) & 31, 32 + 8 * (e & 3), 64)) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
     if (warp == 0) { tmem_alloc(&tbase, 512); tmem_relinquish(); }
     tc_fence_before_sync();
     __syncthreads();
@@ -265,9 +274,15 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // Bounded wait of a whole warp; on expiry the timeout is recorded and the role
     // leaves its loop (the others run into their own limits).
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        const bool r = mbar_wait(bar, parity & 1, globaltimer_ns() + kWaitNs);
-        if (!r) named_timeout(a.status);
-        return __all_sync(0xffffffffu, r) != 0;
+        // The timer is read only once a try has failed: a hand-off that is ready costs
+        // one try_wait.
+        bool r = mbar_try_wait(bar, parity & 1);
+        if (!__all_sync(0xffffffffu, r)) {
+            r = mbar_wait(bar, parity & 1, globaltimer_ns() + kWaitNs);
+            if (!r) named_timeout(a.status);
+            return __all_sync(0xffffffffu, r) != 0;
+        }
+        return true;
     };
 
     if (warp < kIntraWarp) {
@@ -372,21 +387,20 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     } else if (warp < kAuxWarp) {
         // ------------------------------------------------------------- intra --
-        const int it = tid - kChainThreads, wq = warp & 3, half = wq & 1;
-        const int r = it & 63;
+        const int group = (warp - kIntraWarp) >> 2, wq = warp & 3, half = wq & 1;
+        const int it = 32 * wq + lane, r = it & 63;
         const bool is_p = wq >= 2;
-        const bool leader = warp == kIntraWarp && elect_one();
-        float *M = (float *)(sm + kOffA);
+        float *D0 = (float *)(sm + kOffM + group * kMGroup), *D1 = D0 + kMBlock, *X = D1 + kMBlock;
         bool ok = true;
-        // Tiles of chunk c are in shared memory; rows past its last token (another
-        // sequence's, or unwritten ones) become zeros in K and V.
+        // A partial chunk's rows past its last token (another sequence's, or unwritten
+        // ones) become zeros in K and V, before any product reads the tiles.
         auto prepare = [&](int c) {
-            ok = ok && wait(&bars.kq_full[c % kKQStages], c / kKQStages);
             const int m = len_of(c);
             if (m < kC) {
-                ok = ok && wait(&bars.v_full[c % kVStages], c / kVStages);
+                ok = ok && wait(&bars.kq_full[c % kKQStages], c / kKQStages) &&
+                     wait(&bars.v_full[c % kVStages], c / kVStages);
                 uint8_t *kt = sm + (c % kKQStages) * kKQStage, *vt = sm + kOffV + (c % kVStages) * kVStage;
-                for (int e = it; e < (kC - m) * 8; e += kIntraThreads) {
+                for (int e = it; e < (kC - m) * 8; e += kGroupThreads) {
                     const uint32_t at = (uint32_t)(m + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
                     const uint4 zero = make_uint4(0, 0, 0, 0);
                     *(uint4 *)(kt + at) = zero;
@@ -396,197 +410,145 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 fence_proxy_async_smem();
             }
+            mbar_arrive(&bars.prep[c & 1]);
         };
-        auto issue_ap = [&](int c) {
-            const uint32_t st = smem_u32(sm + (c % kKQStages) * kKQStage);
+        if (group < nch) prepare(group);
+        for (int c = group; c < nch; c += 2) {
+            const Gate &gt = gates[c % kKQStages];
+            ok = ok && wait(&bars.gate_full[c % kKQStages], c / kKQStages);
+            if (c >= 2) {   // P's buffer and this group's blocks: read by chunk c - 2's products
+                ok = ok && wait(&bars.o_full[c & 1], (c >> 1) - 1);
+                ok = ok && wait(&bars.w_full[c & 1], (c >> 1) - 1);
+            }
+            const float Gr = gt.G[r], br = is_p ? 1.f : gt.beta[r];
+            // Row factors: the decay from a tile's end to this row (below 1 for earlier
+            // tiles; up to 2^100 for its own, where f undoes it).
+            const float n0 = br * ex2(Gr - gt.G[32 * half + 15]), n1 = br * ex2(Gr - gt.G[32 * half + 31]);
+            const float far0 = half ? br * ex2(Gr - gt.G[15]) : 0.f, far1 = half ? br * ex2(Gr - gt.G[31]) : 0.f;
+            const int lim = (is_p ? r : r - 1) - 32 * half;    // last column kept of the near 32
+            const bool steep = gt.steep != 0;
+            ok = ok && wait(&bars.ap_full[c & 1], c >> 1);
             tc_fence_after_sync();
+            uint8_t *img = sm + kOffP + (c & 1) * 8192;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint64_t d = desc_kmajor_sw128(st + (ks >> 2) * 16384 + (ks & 3) * 32);
-                mma_ss(tmem_addr(tb, 0, kTAP), d, d, idesc_bf16_f32(128, 64), ks > 0);
-            }
-            mma_commit(&bars.ap_full[c & 1]);
-        };
-        prepare(0);
-        if (!intra_sync_any(!ok)) {
-            if (leader) issue_ap(0);
-            __syncwarp();
-            for (int c = 0; c < nch; ++c) {
-                const Gate &gt = gates[c % kKQStages];
-                ok = ok && wait(&bars.gate_full[c % kKQStages], c / kKQStages);
-                ok = ok && wait(&bars.ap_full[c & 1], c >> 1);
-                // P's buffer: free once the outputs of chunk c - 2 are formed.
-                if (c >= 2) ok = ok && wait(&bars.o_full[c & 1], (c >> 1) - 1);
-                tc_fence_after_sync();
-                {
-                    uint32_t va[32], vb[32];
-                    tmem_ld32(tmem_addr(tb, lq, kTAP), va);
-                    if (half) tmem_ld32(tmem_addr(tb, lq, kTAP + 32), vb);
-                    tmem_ld_wait();
-                    const float Gr = gt.G[r], br = is_p ? 1.f : gt.beta[r];
-                    const int lim = is_p ? r : r - 1;    // last column kept
-                    // Columns s0 .. s0 + 31 of the two 16-token tiles that hold this warp's
-                    // rows: one exponent per element.
-                    auto near = [&](uint32_t (&v)[32], int s0) {
+            for (int part = 0; part < 2; ++part) {   // 0: the near 32 columns; 1: columns 0-31 of rows 32-63
+                if (part == 1 && !half) break;
+                uint32_t v[32];
+                const int s0 = part == 0 ? 32 * half : 0;
+                tmem_ld32(tmem_addr(tb, lq, kTAP + s0), v);
+                tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 G4 = *(const float4 *)&gt.G[s0 + i];
-                            const float gs[4] = {G4.x, G4.y, G4.z, G4.w};
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 f4 = *(const float4 *)&gt.f[s0 + i];
+                    const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                v[i + u] = s0 + i + u <= lim
-                                               ? __float_as_uint(__uint_as_float(v[i + u]) * br * ex2(Gr - gs[u]))
-                                               : 0u;
-                        }
-                    };
-                    if (half) {
-                        // Earlier tiles: the token's decay to its tile's end, times the row's
-                        // decay from there.
-                        const float a0 = br * ex2(Gr - gt.G[15]), a1 = br * ex2(Gr - gt.G[31]);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 f4 = *(const float4 *)&gt.f[i];
-                            const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                va[i + u] = __float_as_uint(__uint_as_float(va[i + u]) * ((i < 16 ? a0 : a1) * fs[u]));
-                        }
-                        near(vb, 32);
-                    } else {
-                        near(va, 0);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) vb[i] = 0u;
-                    }
-                    if (is_p) {
-                        uint8_t *img = sm + kOffP + (c & 1) * 8192;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            auto piece = [&](uint32_t (&v)[32], int col) {
-                                uint4 w;
-                                w.x = pack(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
-                                w.y = pack(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
-                                w.z = pack(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
-                                w.w = pack(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
-                                *(uint4 *)(img + sw128_offset(r, col + 8 * i, 64)) = w;
-                            };
-                            piece(va, 0);
-                            piece(vb, 32);
-                        }
-                        fence_proxy_async_smem();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            *(uint4 *)&M[r * kLd + i] = make_uint4(va[i], va[i + 1], va[i + 2], va[i + 3]);
-                            if (half)
-                                *(uint4 *)&M[r * kLd + 32 + i] = make_uint4(vb[i], vb[i + 1], vb[i + 2], vb[i + 3]);
-                        }
+                    for (int u = 0; u < 4; ++u) {
+                        const float row = part == 0 ? (i < 16 ? n0 : n1) : (i < 16 ? far0 : far1);
+                        float x = __uint_as_float(v[i + u]);
+                        if (part == 0 && steep) x = x * br * ex2(Gr - gt.G[s0 + i + u]);
+                        else x = x * (row * fs[u]);
+                        v[i + u] = part == 1 || i + u <= lim ? __float_as_uint(x) : 0u;
                     }
                 }
-                tc_fence_before_sync();
-                if (c + 1 < nch) prepare(c + 1);
-                if (intra_sync_any(!ok)) break;
-                if (leader && c + 1 < nch) issue_ap(c + 1);
+                if (is_p) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 w;
+                        w.x = pack(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
+                        w.y = pack(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
+                        w.z = pack(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
+                        w.w = pack(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
+                        *(uint4 *)(img + sw128_offset(r, s0 + 8 * i, 64)) = w;
+                    }
+                } else {
+                    float *m = (part == 1 ? X : (half ? D1 : D0)) + (r & 31) * kLd;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *(uint4 *)&m[i] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&bars.ap_tfree);
+            // The next chunk of this group: its product may start unless its tiles need zeros.
+            if (c + 2 < nch && len_of(c + 2) == kC) mbar_arrive(&bars.prep[c & 1]);
+            if (group_sync_any(group, !ok)) break;
+            // Inverse of the two 32 x 32 diagonal blocks, one warp each: half a warp solves a
+            // 16 x 16 block, lane j its column j, four unknowns at a time; then the block
+            // between them.
+            if (!is_p) {
+                float *Dw = half ? D1 : D0;
+                float *B = Dw + 16 * (lane >> 4) * (kLd + 1);
+                const int j = lane & 15, g = lane >> 2, t = lane & 3;
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+                for (int m0 = 0; m0 < 16; m0 += 4) {
+#pragma unroll
+                    for (int i = m0 + 1; i < 16; ++i) {
+                        const float4 l = *(const float4 *)&B[i * kLd + m0];
+                        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
+                    }
+                }
                 __syncwarp();
-                // Inverse, level 0: warp w inverts the diagonal block w; lane j solves column
-                // j, four unknowns at a time (both half-warps do the same work).
-                {
-                    float *B = M + 16 * wq * (kLd + 1);
-                    const int j = lane & 15;
-                    float x[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+                for (int i = 0; i < 16; ++i) B[i * kLd + j] = x[i];
+                __syncwarp();
+                float z[2][4];
+                block_product<16, 2>(Dw + 16 * (kLd + 1), Dw + 16 * kLd, Dw, 0, 0, lane, z);
+                __syncwarp();
 #pragma unroll
-                    for (int m0 = 0; m0 < 16; m0 += 4) {
-#pragma unroll
-                        for (int i = m0 + 1; i < 16; ++i) {
-                            const float4 l = *(const float4 *)&B[i * kLd + m0];
-                            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
-                        }
-                    }
-                    __syncwarp();
-                    if (lane < 16) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) B[i * kLd + j] = x[i];
-                    }
-                }
-                intra_sync();
-                // Level 1: blocks (1, 0) and (3, 2), half of the columns per warp.
-                {
-                    const int i0 = 32 * (wq >> 1) + 16, j0 = i0 - 16, g = lane >> 2, t = lane & 3;
-                    float z[1][4];
-                    block_product<16, 1>(M, i0, j0, 0, 8 * half, lane, z);
-                    intra_sync();
-                    float *p = M + (i0 + g) * kLd + j0 + 8 * half + 2 * t;
-                    *(float2 *)p = make_float2(-z[0][0], -z[0][1]);
-                    *(float2 *)(p + 8 * kLd) = make_float2(-z[0][2], -z[0][3]);
-                }
-                intra_sync();
-                // Level 2: rows 32-63, columns 0-31; 16 rows and 16 columns per warp.
-                {
-                    const int rr = 16 * half, n0 = 16 * (wq >> 1), g = lane >> 2, t = lane & 3;
-                    float z[2][4];
-                    block_product<32, 2>(M, 32, 0, rr, n0, lane, z);
-                    intra_sync();
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float *p = M + (32 + rr + g) * kLd + n0 + 8 * q + 2 * t;
-                        *(float2 *)p = make_float2(-z[q][0], -z[q][1]);
-                        *(float2 *)(p + 8 * kLd) = make_float2(-z[q][2], -z[q][3]);
-                    }
-                }
-                intra_sync();
-                // T's operands, free once the products of chunk c - 1 have read them.
-                if (c > 0) {
-                    ok = ok && wait(&bars.w_full, c - 1);
-                    ok = ok && wait(&bars.v_empty[(c - 1) & 1], (c - 1) >> 1);
-                }
-                {
-                    uint8_t *img = sm + (is_p ? kOffT2 : kOffT1);
-                    const float *colf = is_p ? gt.beta : gt.nbe;
-#pragma unroll
-                    for (int s = 0; s < 64; s += 8) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if ((s >> 4) <= (r >> 4)) {
-                            const float4 x = *(const float4 *)&M[r * kLd + s], y = *(const float4 *)&M[r * kLd + s + 4];
-                            const float4 p = *(const float4 *)&colf[s], q = *(const float4 *)&colf[s + 4];
-                            w.x = pack(x.x * p.x, x.y * p.y);
-                            w.y = pack(x.z * p.z, x.w * p.w);
-                            w.z = pack(y.x * q.x, y.y * q.y);
-                            w.w = pack(y.z * q.z, y.w * q.w);
-                        }
-                        *(uint4 *)(img + sw128_offset(r, s, 64)) = w;
-                    }
-                }
-                fence_proxy_async_smem();
-                if (intra_sync_any(!ok)) break;
-                if (warp == kIntraWarp) {
-                    if (leader) mbar_arrive(&bars.t_ready);
-                    if (c > 0) ok = wait(&bars.w_tfree, c - 1);
-                    if (leader && ok) {
-                        tc_fence_after_sync();
-                        const uint32_t kt = smem_u32(sm + (c % kKQStages) * kKQStage);
-                        const uint32_t t1 = smem_u32(sm + kOffT1);
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ss(tmem_addr(tb, 0, kTW), desc_mnmajor_sw128(kt + ks * 2048, 16384),
-                                   desc_kmajor_sw128(t1 + ks * 32), idesc_bf16_f32(128, 64) | kIdescMnA, ks > 0);
-                        mma_commit(&bars.w_full);
-                    }
-                    __syncwarp();
+                for (int q = 0; q < 2; ++q) {
+                    float *p = Dw + (16 + g) * kLd + 8 * q + 2 * t;
+                    *(float2 *)p = make_float2(-z[q][0], -z[q][1]);
+                    *(float2 *)(p + 8 * kLd) = make_float2(-z[q][2], -z[q][3]);
                 }
             }
+            // T's operands: free once the products of chunk c - 1 have read them.
+            if (c > 0) {
+                ok = ok && wait(&bars.w_full[(c - 1) & 1], (c - 1) >> 1);
+                ok = ok && wait(&bars.v_empty[(c - 1) & 1], (c - 1) >> 1);
+            }
+            if (group_sync_any(group, !ok)) break;
+            {   // rows 32-63, columns 0-31: 16 x 16 per warp, straight to the operands
+                const int rr = 16 * half, nc = 16 * (wq >> 1), g = lane >> 2, t = lane & 3;
+                float z[2][4];
+                block_product<32, 2>(D1, X, D0, rr, nc, lane, z);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int col = nc + 8 * q + 2 * t;
+                    const float2 nb = *(const float2 *)&gt.nbe[col], be = *(const float2 *)&gt.beta[col];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t at = sw128_offset(32 + rr + g + 8 * u, col, 64);
+                        *(uint32_t *)(sm + kOffT1 + at) = pack(-z[q][2 * u] * nb.x, -z[q][2 * u + 1] * nb.y);
+                        *(uint32_t *)(sm + kOffT2 + at) = pack(-z[q][2 * u] * be.x, -z[q][2 * u + 1] * be.y);
+                    }
+                }
+            }
+            {   // the diagonal blocks: half of the threads per operand, a row each
+                const float *m = (r < 32 ? D0 : D1) + (r & 31) * kLd;
+                const float *colf = (is_p ? gt.beta : gt.nbe) + (r & 32);
+                uint8_t *to = sm + (is_p ? kOffT2 : kOffT1);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const float4 x = *(const float4 *)&m[i], y = *(const float4 *)&m[i + 4];
+                    const float4 p = *(const float4 *)&colf[i], q = *(const float4 *)&colf[i + 4];
+                    *(uint4 *)(to + sw128_offset(r, (r & 32) + i, 64)) =
+                        make_uint4(pack(x.x * p.x, x.y * p.y), pack(x.z * p.z, x.w * p.w),
+                                   pack(y.x * q.x, y.y * q.y), pack(y.z * q.z, y.w * q.w));
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.t_ready);
+            if (c + 2 < nch && len_of(c + 2) < kC) prepare(c + 2);
         }
-        if (leader) {   // every product of this role has finished before the CTA may exit
-            mma_commit(&bars.drain[0]);
-            mbar_wait(&bars.drain[0], 0, globaltimer_ns() + kWaitNs);
-        }
-        __syncwarp();
     } else if (warp < kIssueWarp) {
         // --------------------------------------------------------------- aux --
-        const int it = tid - kChainThreads - kIntraThreads, wq = warp & 3;
+        const int wq = warp & 3, it = 32 * wq + lane;
         uint8_t *ost = sm + kOffO + 4096 * wq;     // [64 tokens][32 channels] of this warp
         __nv_bfloat16 *o = (__nv_bfloat16 *)a.o;
         uint32_t xa[32], xb[32];
@@ -632,21 +594,22 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const int row = it >> 1;
                 uint8_t *p = sm + s * kKQStage + 8192 + (it & 1) * 16384 + row * 128;
                 const float d = gt.eG[row];
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = *(const uint4 *)(p + ((i ^ (row & 7)) << 4));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    uint4 *q4 = (uint4 *)(p + ((i ^ (row & 7)) << 4));
-                    uint4 w = *q4;
-                    uint32_t *u = (uint32_t *)&w;
+                    uint32_t *u = (uint32_t *)&w[i];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 f = unpack(u[k]);
                         u[k] = pack(f.x * d, f.y * d);
                     }
-                    *q4 = w;
+                    *(uint4 *)(p + ((i ^ (row & 7)) << 4)) = w[i];
                 }
             }
             // W^T (negated) of key channel 32 wq + lane: 64 tokens -> one 128-byte row.
-            ok = wait(&bars.w_full, c);
+            ok = wait(&bars.w_full[c & 1], c >> 1);
             if (!ok) break;
             tc_fence_after_sync();
             tmem_ld32(tmem_addr(tb, lq, kTW), xa);
@@ -686,11 +649,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!wait(&bars.v_full[c & 1], c >> 1) || !wait(&bars.t_ready, c)) return false;
             tc_fence_after_sync();
             if (leader) {
-                const uint32_t vt = smem_u32(sm + kOffV + (c % kVStages) * kVStage);
+                const uint64_t dv = desc_mnmajor_sw128(smem_u32(sm + kOffV + (c % kVStages) * kVStage), 8192);
+                const uint64_t dt = desc_kmajor_sw128(t2);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(tmem_addr(tb, 0, kTE), desc_mnmajor_sw128(vt + ks * 2048, 8192),
-                           desc_kmajor_sw128(t2 + ks * 32), id64 | kIdescMnA, ks > 0);
+                    mma_ss(tmem_addr(tb, 0, kTE), dv + ks * (2048 >> 4), dt + ks * (32 >> 4), id64 | kIdescMnA, ks > 0);
                 mma_commit(&bars.v_empty[c & 1]);
             }
             __syncwarp();
@@ -700,14 +663,15 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int c = 0; c < nch && ok; ++c) {
             const int s = c % kKQStages;
             const uint32_t st = smem_u32(sm + s * kKQStage), sb = tmem_addr(tb, 0, kTSb);
+            const uint64_t dW = desc_mnmajor_sw128(wimg, 16384), dQ = desc_kmajor_sw128(st + 8192);
+            const uint64_t dK = desc_mnmajor_sw128(st, 16384), dP = desc_kmajor_sw128(smem_u32(sm + kOffP + (c & 1) * 8192));
             ok = wait(&bars.kq_full[s], c / kKQStages) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTE), sb + 8 * ks, desc_mnmajor_sw128(wimg + ks * 2048, 16384),
-                           id64 | kIdescMnB, true);
+                    mma_ts(tmem_addr(tb, 0, kTE), sb + 8 * ks, dW + ks * (2048 >> 4), id64 | kIdescMnB, true);
                 mma_commit(&bars.e_full);
             }
             __syncwarp();
@@ -716,8 +680,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTO), sb + 8 * ks,
-                           desc_kmajor_sw128(st + 8192 + (ks >> 2) * 16384 + (ks & 3) * 32), id64, ks > 0);
+                    mma_ts(tmem_addr(tb, 0, kTO), sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
             }
             __syncwarp();
             ok = wait(&bars.e_ready, c) && wait(&bars.decayed, c);
@@ -726,15 +689,13 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTS), tmem_addr(tb, 0, kTEs + 8 * ks),
-                           desc_mnmajor_sw128(st + ks * 2048, 16384), id128 | kIdescMnB, true);
+                    mma_ts(tmem_addr(tb, 0, kTS), tmem_addr(tb, 0, kTEs + 8 * ks), dK + ks * (2048 >> 4),
+                           id128 | kIdescMnB, true);
                 mma_commit(&bars.s_full);
                 mma_commit(&bars.kq_empty[s]);
-                const uint32_t pimg = smem_u32(sm + kOffP + (c & 1) * 8192);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTO), tmem_addr(tb, 0, kTEo + 8 * ks),
-                           desc_kmajor_sw128(pimg + ks * 32), id64, true);
+                    mma_ts(tmem_addr(tb, 0, kTO), tmem_addr(tb, 0, kTEo + 8 * ks), dP + ks * (32 >> 4), id64, true);
                 mma_commit(&bars.o_full[c & 1]);
             }
             __syncwarp();
@@ -743,6 +704,49 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (leader) {
             mma_commit(&bars.drain[1]);
             mbar_wait(&bars.drain[1], 0, globaltimer_ns() + kWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == kIssue2Warp) {
+        // --------------------------------------------- issue: A, P and W --
+        const bool leader = elect_one();
+        const uint32_t t1 = smem_u32(sm + kOffT1);
+        auto issue_ap = [&](int c) {
+            const int s = c % kKQStages;
+            if (!wait(&bars.kq_full[s], c / kKQStages) || !wait(&bars.prep[c & 1], c >> 1)) return false;
+            if (c > 0 && !wait(&bars.ap_tfree, c - 1)) return false;
+            tc_fence_after_sync();
+            if (leader) {
+                const uint64_t d = desc_kmajor_sw128(smem_u32(sm + s * kKQStage));
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint64_t dk = d + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+                    mma_ss(tmem_addr(tb, 0, kTAP), dk, dk, idesc_bf16_f32(128, 64), ks > 0);
+                }
+                mma_commit(&bars.ap_full[c & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = issue_ap(0) && (nch < 2 || issue_ap(1));
+        for (int c = 0; c < nch && ok; ++c) {
+            ok = wait(&bars.t_ready, c) && (c == 0 || wait(&bars.w_tfree, c - 1));
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (leader) {   // [W^T] = K^T (-T Diag(beta e^G))^T
+                const uint64_t dk = desc_mnmajor_sw128(smem_u32(sm + (c % kKQStages) * kKQStage), 16384);
+                const uint64_t dt = desc_kmajor_sw128(t1);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ss(tmem_addr(tb, 0, kTW), dk + ks * (2048 >> 4), dt + ks * (32 >> 4),
+                           idesc_bf16_f32(128, 64) | kIdescMnA, ks > 0);
+                mma_commit(&bars.w_full[c & 1]);
+            }
+            __syncwarp();
+            if (c + 2 < nch) ok = issue_ap(c + 2);
+        }
+        if (leader) {   // every product of this role has finished before the CTA may exit
+            mma_commit(&bars.drain[0]);
+            mbar_wait(&bars.drain[0], 0, globaltimer_ns() + kWaitNs);
         }
         __syncwarp();
     } else {
@@ -760,25 +764,30 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
         };
         fetch(0);
-        int loaded = 0;
+        int kq_loaded = 0, v_loaded = 0;
         for (int c = 0; c < nch; ++c) {
             const int s = c % kKQStages;
             if (c >= kKQStages && !wait(&bars.kq_empty[s], c / kKQStages - 1)) break;
-            if (c >= kVStages && !wait(&bars.v_empty[c & 1], (c >> 1) - 1)) break;
+            const int t0 = tbeg + begin_of(c);
             if (leader) {
-                uint8_t *st = sm + s * kKQStage, *vt = sm + kOffV + (c % kVStages) * kVStage;
-                const int t0 = tbeg + begin_of(c);
+                uint8_t *st = sm + s * kKQStage;
                 mbar_arrive_expect_tx(&bars.kq_full[s], kKQStage);
                 tma_tile(st, &tm_k, 0, hk, t0, &bars.kq_full[s]);
                 tma_tile(st + 16384, &tm_k, 64, hk, t0, &bars.kq_full[s]);
                 tma_tile(st + 8192, &tm_q, 0, hk, t0, &bars.kq_full[s]);
                 tma_tile(st + 24576, &tm_q, 64, hk, t0, &bars.kq_full[s]);
+            }
+            ++kq_loaded;
+            __syncwarp();
+            if (c >= kVStages && !wait(&bars.v_empty[c & 1], (c >> 1) - 1)) break;
+            if (leader) {
+                uint8_t *vt = sm + kOffV + (c % kVStages) * kVStage;
                 mbar_arrive_expect_tx(&bars.v_full[c & 1], kVStage);
                 tma_tile(vt, &tm_v, 0, h, t0, &bars.v_full[c & 1]);
                 tma_tile(vt + 8192, &tm_v, 64, h, t0, &bars.v_full[c & 1]);
             }
+            ++v_loaded;
             __syncwarp();
-            ++loaded;
             // Decay tables: two tokens per lane, an inclusive scan over the warp.
             float x[2];
 #pragma unroll
@@ -801,17 +810,21 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             *(float2 *)&gt.beta[2 * lane] = make_float2(be[0], be[1]);
             *(float2 *)&gt.nbe[2 * lane] = make_float2(-be[0] * e0, -be[1] * e1);
             *(float2 *)&gt.tail[2 * lane] = make_float2(ex2(GC - G0), ex2(GC - G1));
-            if (lane == 0) gt.eGC = ex2(GC);
+            // Factored decays need every tile's range inside the fp32 exponent.
+            const float tile_begin = __shfl_sync(0xffffffffu, G0, lane & 24);
+            const bool steep = __any_sync(0xffffffffu, !(tile_begin - tile_end <= 100.f) || x[0] > 0.f || x[1] > 0.f);
+            if (lane == 0) { gt.eGC = ex2(GC); gt.steep = steep; }
             __syncwarp();
             if (leader) mbar_arrive(&bars.gate_full[s]);
             if (c + 1 < nch) fetch(c + 1);
         }
         // Every tile has landed before the CTA may exit.
-        if (leader)
-            for (int c = max(0, loaded - 2); c < loaded; ++c) {
+        if (leader) {
+            for (int c = max(0, kq_loaded - kKQStages); c < kq_loaded; ++c)
                 mbar_wait(&bars.kq_full[c % kKQStages], (c / kKQStages) & 1, globaltimer_ns() + kWaitNs);
-                mbar_wait(&bars.v_full[c & 1], (c >> 1) & 1, globaltimer_ns() + kWaitNs);
-            }
+            for (int c = max(0, v_loaded - kVStages); c < v_loaded; ++c)
+                mbar_wait(&bars.v_full[c % kVStages], (c / kVStages) & 1, globaltimer_ns() + kWaitNs);
+        }
         __syncwarp();
     }
     tc_fence_before_sync();
