@@ -1,34 +1,38 @@
 // Chunked gated delta rule on tcgen05 tensor cores (bf16 operands, fp32
 // accumulation, dk = dv = 128), one kernel.
 //
-// Within a chunk of 64 tokens (r, s; G the inclusive running log-decay from the
-// chunk start, one number per token) the recurrence unrolls to
-//   A = strictly_lower(Diag(beta) (K K^T) o D),   P = lower((Q K^T) o D),
-//   D_rs = e^{G_r - G_s},   T = (I + A)^{-1},
-//   U = T Diag(beta) V,   W = T Diag(beta e^G) K,   E = U - W S,
-//   O = scale (Diag(e^G) Q S + P E),   S <- e^{G_C} S + (Diag(e^{G_C - G}) K)^T E.
-// Every decay is one scalar per token (pair), so it folds into T's columns, E's
-// columns and Q's rows; K and V enter the products as their TMA tiles.  All
-// factors e^{G_r - G_s}, r >= s, are formed without a reciprocal and are at most
-// 1 for g <= 0.
+// A chunk holds up to 64 tokens (r, s).  With G_r the log-decay accumulated from
+// the chunk's second token to token r (G = 0 at the first), and the incoming state
+// already multiplied by the first token's e^{g}, the unrolled recurrence is
+//   E_r + sum_{s<r} beta_r (k_r . k_s) e^{G_r - G_s} E_s = beta_r (v_r - e^{G_r} S^T k_r),
+//   o_r = scale (e^{G_r} S^T q_r + sum_{s<=r} (q_r . k_s) e^{G_r - G_s} E_s),
+//   S <- e^{G_C} S + sum_s e^{G_C - G_s} k_s E_s^T.
+// In the variables F_r = e^{-G_r} E_r every decay leaves the sums:
+//   T = (I + strictly_lower(Diag(beta) K K^T))^{-1},  P = lower(Q K^T),  W = T Diag(beta) K,
+//   F = T Diag(beta e^{-G}) V - W S,  o_r = scale e^{G_r} (Q S + P F)_r,
+//   S <- e^{G_C} (S + K^T F),
+// so one factor per token remains at T's columns, one at the outputs and one at the
+// state; K, Q and V enter the products as their TMA tiles.  e^{-G} has to stay in the
+// floating-point range: a chunk ends early, before the token at which |G| would pass
+// 2^kRange; below 2^kSafe nothing is shifted, between them the chunk's scale is shifted
+// down so that e^{-G} <= 2^kSafe (state entries below 2^-26 are then lost in that
+// chunk, which multiplies the state by less than 2^-100 anyway).  Relative accuracy
+// is that of the decayed form: each term is scaled by a power it keeps to its use.
 //
-// One CTA of 23 warps owns a (sequence, value head) and walks its chunks with the
-// fp32 state transposed in tensor memory.  Nothing goes through HBM but q, k, v,
-// g, beta, o and the state rows.  Roles:
-//   chain (warps 0-7)    E^T from its accumulator to bf16 operands (E for the
-//                        outputs, e^{G_C - G} E for the state); S^T to its bf16
-//                        copy, then the fp32 master times the next e^{G_C};
-//   intra (warps 8-15)   two groups, even and odd chunks: A and P from the accumulator
-//                        with their decays, T by 16 x 16 forward substitution and two
-//                        block doublings (tf32 mma), T's two bf16 operands;
-//   aux   (warps 16-19)  Q <- e^G Q in place, W^T from its accumulator to a bf16
-//                        operand, O^T to o;
+// One CTA of 24 warps owns a (sequence, value head) and walks its chunks with the fp32
+// state transposed in tensor memory.  Nothing goes through HBM but q, k, v, g, beta,
+// o and the state rows.  Roles:
+//   chain (warps 0-7)    F^T from its accumulator to a bf16 operand; S^T times its
+//                        factor, to the fp32 master and its bf16 copy;
+//   intra (warps 8-15)   two groups, even and odd chunks: A and P from the accumulator,
+//                        T by 16 x 16 forward substitution and two block doublings
+//                        (tf32 mma), T's two bf16 operands;
+//   aux   (warps 16-19)  W^T from its accumulator to a bf16 operand, O^T to o;
 //   issue (warps 20, 21) the products of the state chain; A, P and W's products;
-//   load  (warp 22)      TMA tiles, and the decay tables of a chunk (a warp scan).
+//   load  (warp 22)      chunk bounds and factors (a warp scan), TMA tiles.
 // Products (TMEM accumulators in brackets), chunk c:
-//   [AP] = [K; Q] K^T;  [W^T] = K^T (-T Diag(beta e^G))^T;  [E^T] = V^T (T Diag(beta))^T
-//   [E^T] += S^T (-W)^T;  [O^T] = S^T (e^G Q)^T
-//   [S^T] += (e^{G_C - G} E)^T K;  [O^T] += E^T P^T
+//   [AP] = [K; Q] K^T;  [W^T] = K^T (-T Diag(beta))^T;  [F^T] = V^T (T Diag(beta e^{-G}))^T
+//   [F^T] += S^T (-W)^T;  [O^T] = S^T Q^T;  [S^T] += F^T K;  [O^T] += F^T P^T
 // K^T, V^T and W^T are MN-major operands, so no tile is ever transposed.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,23 +49,28 @@ namespace {
 using namespace tc;
 
 constexpr int kD = 128, kC = 64;              // head size, chunk
-constexpr uint64_t kWaitNs = 2000000000ull;   // per-wait limit: 2 s
+// A wait gives up after kTries tries, each of which sleeps at most kSuspendNs (or until the
+// phase completes): between tens of milliseconds and two seconds, against hand-offs that
+// take microseconds.
+constexpr uint32_t kTries = 1u << 20, kSuspendNs = 2000;
+constexpr uint64_t kDrainNs = 2000000000ull;   // limit of the waits at the end of a role
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRange = 200.f, kSafe = 100.f;   // log2 bounds of e^{-G}, see above
 
 constexpr int kChainThreads = 256, kGroupThreads = 128, kAuxThreads = 128;
 constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kIssue2Warp = 21, kLoadWarp = 22;
-constexpr int kThreads = (kLoadWarp + 1) * 32;
+constexpr int kThreads = 24 * 32;             // whole warpgroups (one warp idles)
 
 // Shared memory (offsets from a 1024-aligned base).  A K/Q stage is
 // [k K0 | q K0 | k K1 | q K1], 8 KiB each (64 rows x 128 B, 128-byte swizzle): the
 // 128-row operand [K; Q] per half of 64 channels.  V: two halves of 8 KiB.
 constexpr uint32_t kKQStage = 32768, kVStage = 16384;
-constexpr int kKQStages = 3, kVStages = 2;
+constexpr int kKQStages = 3, kVStages = 2, kInfos = 8;
 constexpr uint32_t kOffV = kKQStages * kKQStage;
 constexpr uint32_t kOffW = kOffV + kVStages * kVStage;   // W^T: 128 channels x 64 tokens
 constexpr uint32_t kOffP = kOffW + 16384;                // P: 64 x 64, two buffers
-constexpr uint32_t kOffT1 = kOffP + 2 * 8192;            // -T Diag(beta e^G): 64 x 64
-constexpr uint32_t kOffT2 = kOffT1 + 8192;               // T Diag(beta)
+constexpr uint32_t kOffT1 = kOffP + 2 * 8192;            // -T Diag(beta): 64 x 64
+constexpr uint32_t kOffT2 = kOffT1 + 8192;               // T Diag(beta e^{-G})
 constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group: fp32 blocks, see kMBlock
 // A's 32 x 32 diagonal blocks (then T's) and its lower-left block, rows padded to 36.
 constexpr int kLd = 36, kMBlock = 32 * kLd;
@@ -72,33 +81,31 @@ constexpr uint32_t kSmem = kOffO + 4 * 4096 + 1024;
 // TMEM columns.
 constexpr uint32_t kTS = 0;      // S^T, fp32 [dv][dk]
 constexpr uint32_t kTSb = 128;   // its bf16 copy
-constexpr uint32_t kTE = 192;    // E^T accumulator [dv][token]
-constexpr uint32_t kTEo = 256;   // E^T bf16, for the outputs
-constexpr uint32_t kTEs = 288;   // e^{G_C - G} E^T bf16, for the state
+constexpr uint32_t kTF = 192;    // F^T accumulator [dv][token]
+constexpr uint32_t kTFb = 256;   // F^T bf16
 constexpr uint32_t kTO = 320;    // O^T accumulator
 constexpr uint32_t kTAP = 384;   // A and P accumulators (rows 0-63, 64-127)
 constexpr uint32_t kTW = 448;    // W^T accumulator [dk][token]
 
 struct Bars {
-    uint64_t kq_full[kKQStages], kq_empty[kKQStages], gate_full[kKQStages];
-    uint64_t v_full[kVStages], v_empty[kVStages];   // v_empty: E^T = V^T T.. done (T too)
-    uint64_t ap_full[2], o_full[2], w_full[2], prep[2];
+    uint64_t kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos];
+    uint64_t v_full[kVStages], v_empty[kVStages];   // v_empty: the product with V and T is done
+    uint64_t ap_full[2], o_full[2], w_full[2], zeroed[2];
     uint64_t ap_tfree, t_ready, w_tfree, w_ready;
-    uint64_t s_ready, e_ready, decayed, e_full, s_full, o_free;
+    uint64_t s_ready, f_ready, f_full, s_full, o_free;
     uint64_t drain[2];
 };
 
-// Decay tables of a chunk (base-2 logarithms), one per K/Q stage.
-struct __align__(16) Gate {
-    float G[kC];      // running log-decay
-    float f[kC];      // 2^(G at the end of the token's 16-token tile - G)
-    float eG[kC];     // 2^G
-    float beta[kC];
-    float nbe[kC];    // -beta 2^G
-    float tail[kC];   // 2^(G_C - G)
-    float eGC;        // 2^G_C
-    int steep;        // some tile decays by more than 2^-100: no factored form there
-    int pad[2];
+// Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks; the load warp
+// writes chunk c + 2's only when the product with V of chunk c is done, which is behind every
+// read of chunk c - 3's.
+struct __align__(16) Info {
+    float beta[kC];   // 0 past the chunk's last token
+    float ev[kC];     // beta e^{-G}
+    float eo[kC];     // scale e^{G}
+    float in, out;    // factors of the state: before the chunk (first token's e^g), after it (e^{G_C})
+    int start, len;   // first token in the sequence, tokens
+    int last, pad[3];
 };
 
 struct Params {
@@ -116,8 +123,27 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
 }
-__device__ __forceinline__ float2 unpack(uint32_t u) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+// 16 lanes x 64 columns of TMEM as 16 x 8 accumulator tiles: v[4 j ..] holds, of column
+// group 8 j, (lane g, columns 2t, 2t + 1) and (lane g + 8, the same columns), with
+// g = thread / 4, t = thread % 4.
+__device__ __forceinline__ void tmem_ld_tiles(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+// Four 8 x 8 16-bit tiles, each stored transposed; lane 8 m + i gives the address of row i of
+// tile m.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 ::"r"(saddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ uint32_t tf32(float x) {
     uint32_t y;
@@ -150,6 +176,10 @@ __device__ __forceinline__ void tma_tile(void *smem_dst, const CUtensorMap *map,
           "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int h, int t0) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t0) : "memory");
+}
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *smem_src, int x, int h, int t0) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t0), "r"(smem_u32(smem_src))
@@ -161,23 +191,25 @@ __device__ __forceinline__ void named_timeout(int32_t *status) {
 
 // Off-diagonal block of the inverse of a lower-triangular matrix from its inverted diagonal
 // blocks: Z = (T_ii A_ij) T_jj (the caller negates), all blocks W x W with leading dimension
-// kLd.  This warp forms the 16 rows from rr, of them NT 8-column tiles from column n0.
-template <int W, int NT>
+// kLd.  T's blocks are stored rounded to tf32, A too unless ROUND_A (T goes on to bf16, eight
+// times coarser).  This warp forms the 16 rows from rr, of them NT 8-column tiles from column n0.
+template <int W, int NT, bool ROUND_A>
 __device__ __forceinline__ void block_product(const float *Ti, const float *A, const float *Tj, int rr, int n0,
                                               int lane, float (&z)[NT][4]) {
     const int g = lane >> 2, t = lane & 3;
     float y[W / 8][4];
 #pragma unroll
     for (int n = 0; n < W / 8; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < rr + 16; k += 8) {    // T_ii is lower triangular
+        const float *p = Ti + (rr + g) * kLd + k + t, *q = A + (k + t) * kLd + g;
+        const uint32_t a[4] = {__float_as_uint(p[0]), __float_as_uint(p[8 * kLd]), __float_as_uint(p[4]),
+                               __float_as_uint(p[8 * kLd + 4])};
 #pragma unroll
-    for (int k = 0; k < W; k += 8) {
-        if (k >= rr + 16) break;    // T_ii is lower triangular
-        uint32_t a[4];
-        const float *p = Ti + (rr + g) * kLd + k + t;
-        a[0] = tf32(p[0]); a[1] = tf32(p[8 * kLd]); a[2] = tf32(p[4]); a[3] = tf32(p[8 * kLd + 4]);
-        const float *q = A + (k + t) * kLd + g;
-#pragma unroll
-        for (int n = 0; n < W / 8; ++n) mma_tf32(y[n], a, tf32(q[8 * n]), tf32(q[4 * kLd + 8 * n]));
+        for (int n = 0; n < W / 8; ++n) {
+            const float b0 = q[8 * n], b1 = q[4 * kLd + 8 * n];
+            mma_tf32(y[n], a, ROUND_A ? tf32(b0) : __float_as_uint(b0), ROUND_A ? tf32(b1) : __float_as_uint(b1));
+        }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
@@ -189,8 +221,21 @@ __device__ __forceinline__ void block_product(const float *Ti, const float *A, c
         const float *q = Tj + (8 * k + 2 * t) * kLd + n0 + g;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            if (8 * k + 7 >= n0 + 8 * n) mma_tf32(z[n], a, tf32(q[8 * n]), tf32(q[kLd + 8 * n]));
+            if (8 * k + 7 >= n0 + 8 * n)
+                mma_tf32(z[n], a, __float_as_uint(q[8 * n]), __float_as_uint(q[kLd + 8 * n]));
     }
+}
+
+// The rest of a wait whose first try did not succeed.  Not inlined: there are forty waits, and
+// the roles' code has to stay in the instruction cache together.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t *status) {
+    uint64_t *p = (uint64_t *)__cvta_shared_to_generic(bar);
+    bool r = false;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kTries && !r; ++i)
+        r = __all_sync(0xffffffffu, mbar_try_wait_hint(p, parity, kSuspendNs));
+    if (!r) named_timeout(status);
+    return r;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -201,7 +246,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     __shared__ Bars bars;
-    __shared__ Gate gates[kKQStages];
+    __shared__ Info infos[kInfos];
     __shared__ uint32_t tbase;
     const GdrArgs &a = prm.a;
 
@@ -219,31 +264,25 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (dst >= 0 && dst != src) {
             float4 *to = (float4 *)row_of(dst);
             const float4 *from = src >= 0 ? (const float4 *)row_of(src) : nullptr;
+#pragma unroll 1
             for (int e = tid; e < kD * kD / 4; e += kThreads)
                 to[e] = from ? from[e] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         return;
     }
-    // Chunks end at multiples of 64 of the absolute position when block rows are
-    // wanted (block sizes are multiples of 64), so that each block ends a chunk.
-    const int off = a.block > 0 ? ctx % kC : 0;
-    const int nch = (int)(((int64_t)off + len + kC - 1) / kC);
-    auto begin_of = [&](int c) { return c == 0 ? 0 : c * kC - off; };
-    auto len_of = [&](int c) { return min((c + 1) * kC - off, len) - begin_of(c); };
-
     if (tid == 0) {
         for (int s = 0; s < kKQStages; ++s) {
             mbar_init(&bars.kq_full[s], 1);
             mbar_init(&bars.kq_empty[s], 1);
-            mbar_init(&bars.gate_full[s], 1);
         }
+        for (int s = 0; s < kInfos; ++s) mbar_init(&bars.info_full[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
             mbar_init(&bars.ap_full[s], 1);
             mbar_init(&bars.o_full[s], 1);
             mbar_init(&bars.w_full[s], 1);
-            mbar_init(&bars.prep[s], kGroupThreads);
+            mbar_init(&bars.zeroed[s], kGroupThreads);
             mbar_init(&bars.drain[s], 1);
         }
         mbar_init(&bars.ap_tfree, kGroupThreads);
@@ -251,9 +290,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(&bars.w_tfree, kAuxThreads);
         mbar_init(&bars.w_ready, kAuxThreads);
         mbar_init(&bars.s_ready, kChainThreads);
-        mbar_init(&bars.e_ready, kChainThreads);
-        mbar_init(&bars.decayed, kChainThreads);
-        mbar_init(&bars.e_full, 1);
+        mbar_init(&bars.f_ready, kChainThreads);
+        mbar_init(&bars.f_full, 1);
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.o_free, kAuxThreads);
         fence_mbar_init();
@@ -271,119 +309,92 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t tb = tbase;
     const uint32_t lq = 32 * (warp & 3);   // this warp's TMEM lanes
 
-    // Bounded wait of a whole warp; on expiry the timeout is recorded and the role
-    // leaves its loop (the others run into their own limits).
+    // Bounded wait of a whole warp; on expiry the timeout is recorded and the role leaves its
+    // loop (the others run into the same limit).
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        // The timer is read only once a try has failed: a hand-off that is ready costs
-        // one try_wait.
-        bool r = mbar_try_wait(bar, parity & 1);
-        if (!__all_sync(0xffffffffu, r)) {
-            r = mbar_wait(bar, parity & 1, globaltimer_ns() + kWaitNs);
-            if (!r) named_timeout(a.status);
-            return __all_sync(0xffffffffu, r) != 0;
-        }
-        return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity & 1, kSuspendNs))) return true;
+        return wait_slow(smem_u32(bar), parity & 1, a.status);
     };
+    auto wait_info = [&](int c) { return wait(&bars.info_full[c % kInfos], c / kInfos); };
 
     if (warp < kIntraWarp) {
         // ------------------------------------------------------------- chain --
         const int j = tid & 127, hh = warp >> 2;   // value channel; half of tokens / key channels
-        uint32_t ra[32], rb[32];
-        bool ok = wait(&bars.gate_full[0], 0);
         const float *S0 = src >= 0 ? row_of(src) + (size_t)(64 * hh) * kD + j : nullptr;
-#pragma unroll
+        bool ok = wait_info(0);
+#pragma unroll 1
         for (int p = 0; p < 2; ++p) {
             uint32_t x[32], y[16];
+            const float f = infos[0].in;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = S0 ? __float_as_uint(S0[(size_t)(32 * p + i) * kD]) : 0u;
+            for (int i = 0; i < 32; ++i)
+                x[i] = S0 ? __float_as_uint(S0[(size_t)(32 * p + i) * kD] * f) : 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
             tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh + 16 * p), y);
-            const float d = gates[0].eGC;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * d);
             tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
         }
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&bars.s_ready);
-        mbar_arrive(&bars.decayed);
-        for (int c = 0; c < nch && ok; ++c) {
-            // E^T of this half's 32 tokens -> bf16, plain and with the decay to the chunk end.
-            ok = wait(&bars.e_full, c);
+#pragma unroll 1
+        for (int c = 0; ok; ++c) {
+            uint32_t x[32], y[16];
+            const Info &in = infos[c % kInfos];
+            const bool last = in.last != 0;
+            const float out = in.out;
+            const int64_t done = (int64_t)ctx + in.start + in.len;
+            // F^T of this half's 32 tokens -> bf16.
+            ok = wait(&bars.f_full, c);
             if (!ok) break;
             tc_fence_after_sync();
-            tmem_ld32(tmem_addr(tb, lq, kTE + 32 * hh), ra);
+            tmem_ld32(tmem_addr(tb, lq, kTF + 32 * hh), x);
             tmem_ld_wait();
-            {
-                const float4 *tail = (const float4 *)&gates[c % kKQStages].tail[32 * hh];
-                uint32_t eo[16], es[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 d = tail[i];
-                    const float e0 = __uint_as_float(ra[4 * i]), e1 = __uint_as_float(ra[4 * i + 1]);
-                    const float e2 = __uint_as_float(ra[4 * i + 2]), e3 = __uint_as_float(ra[4 * i + 3]);
-                    es[2 * i] = pack(e0 * d.x, e1 * d.y);
-                    es[2 * i + 1] = pack(e2 * d.z, e3 * d.w);
-                    eo[2 * i] = pack(e0, e1);
-                    eo[2 * i + 1] = pack(e2, e3);
-                }
-                tmem_st16(tmem_addr(tb, lq, kTEs + 16 * hh), es);
-                tmem_st16(tmem_addr(tb, lq, kTEo + 16 * hh), eo);
-            }
+            for (int i = 0; i < 16; ++i) y[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            tmem_st16(tmem_addr(tb, lq, kTFb + 16 * hh), y);
             tmem_st_wait();
             tc_fence_before_sync();
-            mbar_arrive(&bars.e_ready);
-            ok = wait(&bars.s_full, c);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const bool last = c + 1 == nch;
-            tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh), ra);
-            tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32), rb);
-            tmem_ld_wait();
-            if (!last) {
-                uint32_t y[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = pack(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1]));
-                tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh), y);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = pack(__uint_as_float(rb[2 * i]), __uint_as_float(rb[2 * i + 1]));
-                tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh + 16), y);
-                tmem_st_wait();
-                tc_fence_before_sync();
-                mbar_arrive(&bars.s_ready);
-            }
-            // State rows: a block that ends here, and the last state.
-            const int64_t done = (int64_t)ctx + begin_of(c) + len_of(c);
+            mbar_arrive(&bars.f_ready);
+            // Rows that keep the state after this chunk: a block that ends here, the last state.
             int row = -1;
             if (a.block > 0 && done % a.block == 0 && done / a.block <= a.table_cols)
                 row = a.table[(size_t)n * a.table_cols + done / a.block - 1];
             if (row >= a.pool_size) row = -1;
-            for (int w = 0; w < 2; ++w) {
-                const int to = w == 0 ? row : (last ? dst : -1);
-                if (to < 0) continue;
-                float *Sf = row_of(to) + (size_t)(64 * hh) * kD + j;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    Sf[(size_t)i * kD] = __uint_as_float(ra[i]);
-                    Sf[(size_t)(32 + i) * kD] = __uint_as_float(rb[i]);
-                }
-            }
-            if (last) break;
-            // Off the critical path: the master times the next chunk's decay.
-            ok = wait(&bars.gate_full[(c + 1) % kKQStages], (c + 1) / kKQStages);
+            if (!last) ok = wait_info(c + 1);
+            const float f = last ? 0.f : out * infos[(c + 1) % kInfos].in;
+            ok = ok && wait(&bars.s_full, c);
             if (!ok) break;
-            const float d = gates[(c + 1) % kKQStages].eGC;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) {
+                tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
+                tmem_ld_wait();
+                if (row >= 0 || last) {
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w) {
+                        const int to = w == 0 ? row : (last ? dst : -1);
+                        if (to < 0) continue;
+                        float *Sf = row_of(to) + (size_t)(64 * hh + 32 * p) * kD + j;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                ra[i] = __float_as_uint(__uint_as_float(ra[i]) * d);
-                rb[i] = __float_as_uint(__uint_as_float(rb[i]) * d);
+                        for (int i = 0; i < 32; ++i) Sf[(size_t)i * kD] = __uint_as_float(x[i]) * out;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 v = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                                make_float2(f, f));
+                    x[2 * i] = __float_as_uint(v.x);
+                    x[2 * i + 1] = __float_as_uint(v.y);
+                    y[i] = pack(v.x, v.y);
+                }
+                tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh + 16 * p), y);
+                tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
             }
-            tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh), ra);
-            tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32), rb);
             tmem_st_wait();
+            if (last) break;
             tc_fence_before_sync();
-            mbar_arrive(&bars.decayed);
+            mbar_arrive(&bars.s_ready);
         }
     } else if (warp < kAuxWarp) {
         // ------------------------------------------------------------- intra --
@@ -392,16 +403,21 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool is_p = wq >= 2;
         float *D0 = (float *)(sm + kOffM + group * kMGroup), *D1 = D0 + kMBlock, *X = D1 + kMBlock;
         bool ok = true;
-        // A partial chunk's rows past its last token (another sequence's, or unwritten
-        // ones) become zeros in K and V, before any product reads the tiles.
-        auto prepare = [&](int c) {
-            const int m = len_of(c);
-            if (m < kC) {
+        if (group == 1) ok = wait_info(0);
+        bool more = group == 0 || (ok && !infos[0].last);
+#pragma unroll 1
+        for (int c = group; more; c += 2) {
+            ok = ok && wait_info(c);
+            const Info &in = infos[c % kInfos];
+            if (in.len < kC) {
+                // Rows past the last token (another sequence's, or unwritten ones) become zeros
+                // in K and V, before any product reads the tiles.
                 ok = ok && wait(&bars.kq_full[c % kKQStages], c / kKQStages) &&
                      wait(&bars.v_full[c % kVStages], c / kVStages);
                 uint8_t *kt = sm + (c % kKQStages) * kKQStage, *vt = sm + kOffV + (c % kVStages) * kVStage;
-                for (int e = it; e < (kC - m) * 8; e += kGroupThreads) {
-                    const uint32_t at = (uint32_t)(m + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
+#pragma unroll 1
+                for (int e = it; e < (kC - in.len) * 8; e += kGroupThreads) {
+                    const uint32_t at = (uint32_t)(in.len + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
                     const uint4 zero = make_uint4(0, 0, 0, 0);
                     *(uint4 *)(kt + at) = zero;
                     *(uint4 *)(kt + 16384 + at) = zero;
@@ -409,69 +425,62 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     *(uint4 *)(vt + 8192 + at) = zero;
                 }
                 fence_proxy_async_smem();
+                mbar_arrive(&bars.zeroed[group]);
             }
-            mbar_arrive(&bars.prep[c & 1]);
-        };
-        if (group < nch) prepare(group);
-        for (int c = group; c < nch; c += 2) {
-            const Gate &gt = gates[c % kKQStages];
-            ok = ok && wait(&bars.gate_full[c % kKQStages], c / kKQStages);
-            if (c >= 2) {   // P's buffer and this group's blocks: read by chunk c - 2's products
-                ok = ok && wait(&bars.o_full[c & 1], (c >> 1) - 1);
-                ok = ok && wait(&bars.w_full[c & 1], (c >> 1) - 1);
-            }
-            const float Gr = gt.G[r], br = is_p ? 1.f : gt.beta[r];
-            // Row factors: the decay from a tile's end to this row (below 1 for earlier
-            // tiles; up to 2^100 for its own, where f undoes it).
-            const float n0 = br * ex2(Gr - gt.G[32 * half + 15]), n1 = br * ex2(Gr - gt.G[32 * half + 31]);
-            const float far0 = half ? br * ex2(Gr - gt.G[15]) : 0.f, far1 = half ? br * ex2(Gr - gt.G[31]) : 0.f;
-            const int lim = (is_p ? r : r - 1) - 32 * half;    // last column kept of the near 32
-            const bool steep = gt.steep != 0;
+            // This group's blocks: every thread has read chunk c - 2's.
+            if (c >= 2) ok = ok && wait(&bars.w_full[c & 1], (c >> 1) - 1);
+            const float br = in.beta[r];
             ok = ok && wait(&bars.ap_full[c & 1], c >> 1);
             tc_fence_after_sync();
-            uint8_t *img = sm + kOffP + (c & 1) * 8192;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {   // 0: the near 32 columns; 1: columns 0-31 of rows 32-63
-                if (part == 1 && !half) break;
+            uint32_t near[16], far[16];    // P's row, packed (A goes straight to its blocks)
+            {                              // columns 32 half .. + 31, up to the diagonal
                 uint32_t v[32];
-                const int s0 = part == 0 ? 32 * half : 0;
-                tmem_ld32(tmem_addr(tb, lq, kTAP + s0), v);
+                tmem_ld32(tmem_addr(tb, lq, kTAP + 32 * half), v);
                 tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 f4 = *(const float4 *)&gt.f[s0 + i];
-                    const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float row = part == 0 ? (i < 16 ? n0 : n1) : (i < 16 ? far0 : far1);
-                        float x = __uint_as_float(v[i + u]);
-                        if (part == 0 && steep) x = x * br * ex2(Gr - gt.G[s0 + i + u]);
-                        else x = x * (row * fs[u]);
-                        v[i + u] = part == 1 || i + u <= lim ? __float_as_uint(x) : 0u;
-                    }
-                }
+                const int lim = (is_p ? r : r - 1) - 32 * half;   // last column kept
                 if (is_p) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 w;
-                        w.x = pack(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
-                        w.y = pack(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
-                        w.z = pack(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
-                        w.w = pack(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
-                        *(uint4 *)(img + sw128_offset(r, s0 + 8 * i, 64)) = w;
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = i <= lim ? v[i] : 0u;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) near[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                 } else {
-                    float *m = (part == 1 ? X : (half ? D1 : D0)) + (r & 31) * kLd;
+                    float *m = (half ? D1 : D0) + (r & 31) * kLd;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = i <= lim ? __float_as_uint(__uint_as_float(v[i]) * br) : 0u;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) *(uint4 *)&m[i] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+            if (half) {                    // columns 0-31 of rows 32-63
+                uint32_t v[32];
+                tmem_ld32(tmem_addr(tb, lq, kTAP), v);
+                tmem_ld_wait();
+                if (is_p) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) far[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                } else {
+                    float *m = X + (r & 31) * kLd;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
-                        *(uint4 *)&m[i] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        *(uint4 *)&m[i] = make_uint4(tf32(__uint_as_float(v[i]) * br), tf32(__uint_as_float(v[i + 1]) * br),
+                                                     tf32(__uint_as_float(v[i + 2]) * br), tf32(__uint_as_float(v[i + 3]) * br));
                 }
             }
             tc_fence_before_sync();
             mbar_arrive(&bars.ap_tfree);
-            // The next chunk of this group: its product may start unless its tiles need zeros.
-            if (c + 2 < nch && len_of(c + 2) == kC) mbar_arrive(&bars.prep[c & 1]);
             if (group_sync_any(group, !ok)) break;
+            if (is_p) {   // P's buffer: read by the outputs of chunk c - 2
+                if (c >= 2) ok = ok && wait(&bars.o_full[c & 1], (c >> 1) - 1);
+                uint8_t *img = sm + kOffP + (c & 1) * 8192;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    *(uint4 *)(img + sw128_offset(r, 32 * half + 8 * i, 64)) =
+                        make_uint4(near[4 * i], near[4 * i + 1], near[4 * i + 2], near[4 * i + 3]);
+                    if (half)
+                        *(uint4 *)(img + sw128_offset(r, 8 * i, 64)) =
+                            make_uint4(far[4 * i], far[4 * i + 1], far[4 * i + 2], far[4 * i + 3]);
+                }
+            }
             // Inverse of the two 32 x 32 diagonal blocks, one warp each: half a warp solves a
             // 16 x 16 block, lane j its column j, four unknowns at a time; then the block
             // between them.
@@ -495,16 +504,16 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) B[i * kLd + j] = x[i];
+                for (int i = 0; i < 16; ++i) B[i * kLd + j] = __uint_as_float(tf32(x[i]));
                 __syncwarp();
                 float z[2][4];
-                block_product<16, 2>(Dw + 16 * (kLd + 1), Dw + 16 * kLd, Dw, 0, 0, lane, z);
+                block_product<16, 2, true>(Dw + 16 * (kLd + 1), Dw + 16 * kLd, Dw, 0, 0, lane, z);
                 __syncwarp();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float *p = Dw + (16 + g) * kLd + 8 * q + 2 * t;
-                    *(float2 *)p = make_float2(-z[q][0], -z[q][1]);
-                    *(float2 *)(p + 8 * kLd) = make_float2(-z[q][2], -z[q][3]);
+                    *(uint2 *)p = make_uint2(tf32(-z[q][0]), tf32(-z[q][1]));
+                    *(uint2 *)(p + 8 * kLd) = make_uint2(tf32(-z[q][2]), tf32(-z[q][3]));
                 }
             }
             // T's operands: free once the products of chunk c - 1 have read them.
@@ -516,27 +525,30 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             {   // rows 32-63, columns 0-31: 16 x 16 per warp, straight to the operands
                 const int rr = 16 * half, nc = 16 * (wq >> 1), g = lane >> 2, t = lane & 3;
                 float z[2][4];
-                block_product<32, 2>(D1, X, D0, rr, nc, lane, z);
+                block_product<32, 2, false>(D1, X, D0, rr, nc, lane, z);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int col = nc + 8 * q + 2 * t;
-                    const float2 nb = *(const float2 *)&gt.nbe[col], be = *(const float2 *)&gt.beta[col];
+                    const float2 be = *(const float2 *)&in.beta[col], ev = *(const float2 *)&in.ev[col];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const uint32_t at = sw128_offset(32 + rr + g + 8 * u, col, 64);
-                        *(uint32_t *)(sm + kOffT1 + at) = pack(-z[q][2 * u] * nb.x, -z[q][2 * u + 1] * nb.y);
-                        *(uint32_t *)(sm + kOffT2 + at) = pack(-z[q][2 * u] * be.x, -z[q][2 * u + 1] * be.y);
+                        *(uint32_t *)(sm + kOffT1 + at) = pack(z[q][2 * u] * be.x, z[q][2 * u + 1] * be.y);
+                        *(uint32_t *)(sm + kOffT2 + at) = pack(-z[q][2 * u] * ev.x, -z[q][2 * u + 1] * ev.y);
                     }
                 }
             }
             {   // the diagonal blocks: half of the threads per operand, a row each
                 const float *m = (r < 32 ? D0 : D1) + (r & 31) * kLd;
-                const float *colf = (is_p ? gt.beta : gt.nbe) + (r & 32);
+                const float *colf = (is_p ? in.ev : in.beta) + (r & 32);
+                const float sign = is_p ? 1.f : -1.f;
                 uint8_t *to = sm + (is_p ? kOffT2 : kOffT1);
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
                     const float4 x = *(const float4 *)&m[i], y = *(const float4 *)&m[i + 4];
-                    const float4 p = *(const float4 *)&colf[i], q = *(const float4 *)&colf[i + 4];
+                    float4 p = *(const float4 *)&colf[i], q = *(const float4 *)&colf[i + 4];
+                    p.x *= sign; p.y *= sign; p.z *= sign; p.w *= sign;
+                    q.x *= sign; q.y *= sign; q.z *= sign; q.w *= sign;
                     *(uint4 *)(to + sw128_offset(r, (r & 32) + i, 64)) =
                         make_uint4(pack(x.x * p.x, x.y * p.y), pack(x.z * p.z, x.w * p.w),
                                    pack(y.x * q.x, y.y * q.y), pack(y.z * q.z, y.w * q.w));
@@ -544,30 +556,41 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars.t_ready);
-            if (c + 2 < nch && len_of(c + 2) < kC) prepare(c + 2);
+            more = !in.last;
+            if (more) {
+                ok = ok && wait_info(c + 1);
+                more = ok && !infos[(c + 1) % kInfos].last;
+            }
         }
     } else if (warp < kIssueWarp) {
         // --------------------------------------------------------------- aux --
         const int wq = warp & 3, it = 32 * wq + lane;
         uint8_t *ost = sm + kOffO + 4096 * wq;     // [64 tokens][32 channels] of this warp
         __nv_bfloat16 *o = (__nv_bfloat16 *)a.o;
+        const uint32_t osa = smem_u32(ost) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
         uint32_t xa[32], xb[32];
         auto output = [&](int c) {
+            const Info &in = infos[c % kInfos];
             if (!wait(&bars.o_full[c & 1], c >> 1)) return false;
             tc_fence_after_sync();
-            tmem_ld32(tmem_addr(tb, lq, kTO), xa);
-            tmem_ld32(tmem_addr(tb, lq, kTO + 32), xb);
+            tmem_ld_tiles(tmem_addr(tb, lq, kTO), xa);
+            tmem_ld_tiles(tmem_addr(tb, lq + 16, kTO), xb);
             tmem_ld_wait();
             tc_fence_before_sync();
             mbar_arrive(&bars.o_free);
-            const int m = len_of(c), t0 = tbeg + begin_of(c);
+            const int m = in.len, t0 = tbeg + in.start;
             if (lane == 0) bulk_wait_read<0>();    // the previous chunk's store has read the tile
             __syncwarp();
-            __nv_bfloat16 *ot = (__nv_bfloat16 *)ost + lane;
+            // Eight tokens at a time: four 8 x 8 tiles (channels x tokens) become eight token
+            // rows of 32 channels; 16-byte pieces swizzled by token pair against conflicts.
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                ot[i * 32] = __float2bfloat16_rn(a.scale * __uint_as_float(xa[i]));
-                ot[(i + 32) * 32] = __float2bfloat16_rn(a.scale * __uint_as_float(xb[i]));
+            for (int j = 0; j < 8; ++j) {
+                const float2 d = *(const float2 *)&in.eo[8 * j + 2 * (lane & 3)];
+                auto scaled = [&](const uint32_t *x) {
+                    return pack(__uint_as_float(x[0]) * d.x, __uint_as_float(x[1]) * d.y);
+                };
+                stmatrix4_trans(osa + j * 512, scaled(xa + 4 * j), scaled(xa + 4 * j + 2), scaled(xb + 4 * j),
+                                scaled(xb + 4 * j + 2));
             }
             if (m == kC) {
                 fence_proxy_async_smem();
@@ -575,41 +598,23 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (lane == 0) { tma_store(&tm_o, ost, 32 * wq, h, t0); bulk_commit(); }
             } else {       // a partial chunk: only its own rows
                 __syncwarp();
+#pragma unroll 1
                 for (int e = lane; e < m * 4; e += 32)
                     *(uint4 *)(o + ((size_t)(t0 + (e >> 2)) * a.H + h) * kD + 32 * wq + 8 * (e & 3)) =
-                        *(const uint4 *)(ost + e * 16);
+                        *(const uint4 *)(ost + (e >> 2) * 64 + (((e & 3) ^ ((e >> 3) & 3)) << 4));
                 __syncwarp();
             }
             return true;
         };
         bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
-            const int s = c % kKQStages;
-            const Gate &gt = gates[s];
-            // Q <- e^G Q in place, once A and P have read the raw tile.
-            ok = wait(&bars.gate_full[s], c / kKQStages) && wait(&bars.kq_full[s], c / kKQStages) &&
-                 wait(&bars.ap_full[c & 1], c >> 1);
-            if (!ok) break;
-            {
-                const int row = it >> 1;
-                uint8_t *p = sm + s * kKQStage + 8192 + (it & 1) * 16384 + row * 128;
-                const float d = gt.eG[row];
-                uint4 w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = *(const uint4 *)(p + ((i ^ (row & 7)) << 4));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t *u = (uint32_t *)&w[i];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = unpack(u[k]);
-                        u[k] = pack(f.x * d, f.y * d);
-                    }
-                    *(uint4 *)(p + ((i ^ (row & 7)) << 4)) = w[i];
-                }
-            }
+#pragma unroll 1
+        for (int c = 0; ok; ++c) {
+            const bool chunk = c == 0 || !infos[(c - 1) % kInfos].last;
+            if (chunk) {
+                ok = wait_info(c);
+                if (!ok) break;
             // W^T (negated) of key channel 32 wq + lane: 64 tokens -> one 128-byte row.
-            ok = wait(&bars.w_full[c & 1], c >> 1);
+            ok = ok && wait(&bars.w_full[c & 1], c >> 1);
             if (!ok) break;
             tc_fence_after_sync();
             tmem_ld32(tmem_addr(tb, lq, kTW), xa);
@@ -617,158 +622,177 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_ld_wait();
             tc_fence_before_sync();
             mbar_arrive(&bars.w_tfree);
-            if (c > 0) ok = wait(&bars.e_full, c - 1);   // the image: read by chunk c - 1's product
+            if (c > 0) ok = wait(&bars.f_full, c - 1);   // the image: read by chunk c - 1's product
             if (!ok) break;
+            auto piece = [&](const uint32_t *x, int col) {
+                *(uint4 *)(sm + kOffW + sw128_offset(it, col, 128)) =
+                    make_uint4(pack(__uint_as_float(x[0]), __uint_as_float(x[1])), pack(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                               pack(__uint_as_float(x[4]), __uint_as_float(x[5])), pack(__uint_as_float(x[6]), __uint_as_float(x[7])));
+            };
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint4 w;
-                w.x = pack(__uint_as_float(xa[8 * i]), __uint_as_float(xa[8 * i + 1]));
-                w.y = pack(__uint_as_float(xa[8 * i + 2]), __uint_as_float(xa[8 * i + 3]));
-                w.z = pack(__uint_as_float(xa[8 * i + 4]), __uint_as_float(xa[8 * i + 5]));
-                w.w = pack(__uint_as_float(xa[8 * i + 6]), __uint_as_float(xa[8 * i + 7]));
-                *(uint4 *)(sm + kOffW + sw128_offset(it, 8 * i, 128)) = w;
-                w.x = pack(__uint_as_float(xb[8 * i]), __uint_as_float(xb[8 * i + 1]));
-                w.y = pack(__uint_as_float(xb[8 * i + 2]), __uint_as_float(xb[8 * i + 3]));
-                w.z = pack(__uint_as_float(xb[8 * i + 4]), __uint_as_float(xb[8 * i + 5]));
-                w.w = pack(__uint_as_float(xb[8 * i + 6]), __uint_as_float(xb[8 * i + 7]));
-                *(uint4 *)(sm + kOffW + sw128_offset(it, 32 + 8 * i, 128)) = w;
-            }
+            for (int i = 0; i < 4; ++i) { piece(xa + 8 * i, 8 * i); piece(xb + 8 * i, 32 + 8 * i); }
             fence_proxy_async_smem();
             mbar_arrive(&bars.w_ready);
+            }
             if (c > 0) ok = output(c - 1);
+            if (!chunk) break;
         }
-        if (ok) output(nch - 1);
         if (lane == 0) bulk_wait<0>();   // every store has completed before the CTA exits
         __syncwarp();
-    } else if (warp == kIssueWarp) {
+    } else {
+    if (warp == kIssueWarp) {
         // ------------------------------------------------------------- issue --
         const bool leader = elect_one();
         const uint32_t id64 = idesc_bf16_f32(128, 64), id128 = idesc_bf16_f32(128, 128);
-        const uint32_t wimg = smem_u32(sm + kOffW), t2 = smem_u32(sm + kOffT2);
-        auto issue_u = [&](int c) {       // [E^T] = V^T (T Diag(beta))^T
-            if (!wait(&bars.v_full[c & 1], c >> 1) || !wait(&bars.t_ready, c)) return false;
-            tc_fence_after_sync();
-            if (leader) {
-                const uint64_t dv = desc_mnmajor_sw128(smem_u32(sm + kOffV + (c % kVStages) * kVStage), 8192);
-                const uint64_t dt = desc_kmajor_sw128(t2);
+        const uint64_t dW = desc_mnmajor_sw128(smem_u32(sm + kOffW), 16384);
+        const uint64_t dT = desc_kmajor_sw128(smem_u32(sm + kOffT2));
+        const uint32_t sb = tmem_addr(tb, 0, kTSb), fb = tmem_addr(tb, 0, kTFb);
+        bool ok = true, more = true;
+#pragma unroll 1
+        for (int c = -1; ok; ++c) {
+            if (c >= 0) {
+                const int s = c % kKQStages;
+                const uint32_t st = smem_u32(sm + s * kKQStage);
+                const uint64_t dQ = desc_kmajor_sw128(st + 8192), dK = desc_mnmajor_sw128(st, 16384);
+                const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + (c & 1) * 8192));
+                ok = wait(&bars.kq_full[s], c / kKQStages) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (leader) {   // [F^T] += S^T (-W)^T
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(tmem_addr(tb, 0, kTE), dv + ks * (2048 >> 4), dt + ks * (32 >> 4), id64 | kIdescMnA, ks > 0);
-                mma_commit(&bars.v_empty[c & 1]);
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tmem_addr(tb, 0, kTF), sb + 8 * ks, dW + ks * (2048 >> 4), id64 | kIdescMnB, true);
+                    mma_commit(&bars.f_full);
+                }
+                __syncwarp();
+                if (c > 0 && !wait(&bars.o_free, c - 1)) break;
+                tc_fence_after_sync();
+                if (leader) {   // [O^T] = S^T Q^T
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tmem_addr(tb, 0, kTO), sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
+                }
+                __syncwarp();
+                ok = wait(&bars.f_ready, c);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (leader) {   // [S^T] += F^T K;  [O^T] += F^T P^T
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts(tmem_addr(tb, 0, kTS), fb + 8 * ks, dK + ks * (2048 >> 4), id128 | kIdescMnB, true);
+                    mma_commit(&bars.s_full);
+                    mma_commit(&bars.kq_empty[s]);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts(tmem_addr(tb, 0, kTO), fb + 8 * ks, dP + ks * (32 >> 4), id64, true);
+                    mma_commit(&bars.o_full[c & 1]);
+                }
+                __syncwarp();
+                more = !infos[c % kInfos].last;
             }
-            __syncwarp();
-            return true;
-        };
-        bool ok = issue_u(0);
-        for (int c = 0; c < nch && ok; ++c) {
-            const int s = c % kKQStages;
-            const uint32_t st = smem_u32(sm + s * kKQStage), sb = tmem_addr(tb, 0, kTSb);
-            const uint64_t dW = desc_mnmajor_sw128(wimg, 16384), dQ = desc_kmajor_sw128(st + 8192);
-            const uint64_t dK = desc_mnmajor_sw128(st, 16384), dP = desc_kmajor_sw128(smem_u32(sm + kOffP + (c & 1) * 8192));
-            ok = wait(&bars.kq_full[s], c / kKQStages) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
+            if (!more) break;
+            // [F^T] = V^T (T Diag(beta e^{-G}))^T of the next chunk.
+            const int d = c + 1;
+            ok = wait_info(d) && wait(&bars.v_full[d & 1], d >> 1) && wait(&bars.t_ready, d);
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTE), sb + 8 * ks, dW + ks * (2048 >> 4), id64 | kIdescMnB, true);
-                mma_commit(&bars.e_full);
-            }
-            __syncwarp();
-            if (c > 0 && !wait(&bars.o_free, c - 1)) break;
-            tc_fence_after_sync();
-            if (leader) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTO), sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
-            }
-            __syncwarp();
-            ok = wait(&bars.e_ready, c) && wait(&bars.decayed, c);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (leader) {
+                const uint64_t dv = desc_mnmajor_sw128(smem_u32(sm + kOffV + (d % kVStages) * kVStage), 8192);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTS), tmem_addr(tb, 0, kTEs + 8 * ks), dK + ks * (2048 >> 4),
-                           id128 | kIdescMnB, true);
-                mma_commit(&bars.s_full);
-                mma_commit(&bars.kq_empty[s]);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tmem_addr(tb, 0, kTO), tmem_addr(tb, 0, kTEo + 8 * ks), dP + ks * (32 >> 4), id64, true);
-                mma_commit(&bars.o_full[c & 1]);
+                    mma_ss(tmem_addr(tb, 0, kTF), dv + ks * (2048 >> 4), dT + ks * (32 >> 4), id64 | kIdescMnA, ks > 0);
+                mma_commit(&bars.v_empty[d & 1]);
             }
             __syncwarp();
-            if (c + 1 < nch) ok = issue_u(c + 1);
         }
         if (leader) {
             mma_commit(&bars.drain[1]);
-            mbar_wait(&bars.drain[1], 0, globaltimer_ns() + kWaitNs);
+            mbar_wait(&bars.drain[1], 0, globaltimer_ns() + kDrainNs);
         }
         __syncwarp();
     } else if (warp == kIssue2Warp) {
         // --------------------------------------------- issue: A, P and W --
         const bool leader = elect_one();
-        const uint32_t t1 = smem_u32(sm + kOffT1);
-        auto issue_ap = [&](int c) {
-            const int s = c % kKQStages;
-            if (!wait(&bars.kq_full[s], c / kKQStages) || !wait(&bars.prep[c & 1], c >> 1)) return false;
-            if (c > 0 && !wait(&bars.ap_tfree, c - 1)) return false;
-            tc_fence_after_sync();
-            if (leader) {
-                const uint64_t d = desc_kmajor_sw128(smem_u32(sm + s * kKQStage));
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint64_t dk = d + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
-                    mma_ss(tmem_addr(tb, 0, kTAP), dk, dk, idesc_bf16_f32(128, 64), ks > 0);
+        const uint64_t dT = desc_kmajor_sw128(smem_u32(sm + kOffT1));
+        int zeros[2] = {0, 0};     // partial chunks of each group so far
+        bool ok = true, more = true;
+#pragma unroll 1
+        for (int c = -1; ok; ++c) {   // A and P a chunk ahead of W
+            if (more) {               // [AP] = [K; Q] K^T
+                const int d = c + 1, s = d % kKQStages;
+                ok = wait_info(d) && wait(&bars.kq_full[s], d / kKQStages);
+                if (ok && infos[d % kInfos].len < kC) {
+                    const int g = d & 1;
+                    ok = wait(&bars.zeroed[g], g ? zeros[1] : zeros[0]);
+                    if (g) ++zeros[1]; else ++zeros[0];
                 }
-                mma_commit(&bars.ap_full[c & 1]);
+                if (d > 0) ok = ok && wait(&bars.ap_tfree, d - 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (leader) {
+                    const uint64_t dKQ = desc_kmajor_sw128(smem_u32(sm + s * kKQStage));
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint64_t x = dKQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+                        mma_ss(tmem_addr(tb, 0, kTAP), x, x, idesc_bf16_f32(128, 64), ks > 0);
+                    }
+                    mma_commit(&bars.ap_full[d & 1]);
+                }
+                __syncwarp();
+                more = !infos[d % kInfos].last;
             }
-            __syncwarp();
-            return true;
-        };
-        bool ok = issue_ap(0) && (nch < 2 || issue_ap(1));
-        for (int c = 0; c < nch && ok; ++c) {
+            if (c < 0) continue;
             ok = wait(&bars.t_ready, c) && (c == 0 || wait(&bars.w_tfree, c - 1));
             if (!ok) break;
             tc_fence_after_sync();
-            if (leader) {   // [W^T] = K^T (-T Diag(beta e^G))^T
-                const uint64_t dk = desc_mnmajor_sw128(smem_u32(sm + (c % kKQStages) * kKQStage), 16384);
-                const uint64_t dt = desc_kmajor_sw128(t1);
+            if (leader) {   // [W^T] = K^T (-T Diag(beta))^T
+                const uint64_t dK = desc_mnmajor_sw128(smem_u32(sm + (c % kKQStages) * kKQStage), 16384);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(tmem_addr(tb, 0, kTW), dk + ks * (2048 >> 4), dt + ks * (32 >> 4),
+                    mma_ss(tmem_addr(tb, 0, kTW), dK + ks * (2048 >> 4), dT + ks * (32 >> 4),
                            idesc_bf16_f32(128, 64) | kIdescMnA, ks > 0);
                 mma_commit(&bars.w_full[c & 1]);
             }
             __syncwarp();
-            if (c + 2 < nch) ok = issue_ap(c + 2);
+            if (infos[c % kInfos].last) break;
         }
         if (leader) {   // every product of this role has finished before the CTA may exit
             mma_commit(&bars.drain[0]);
-            mbar_wait(&bars.drain[0], 0, globaltimer_ns() + kWaitNs);
+            mbar_wait(&bars.drain[0], 0, globaltimer_ns() + kDrainNs);
         }
         __syncwarp();
-    } else {
+    } else if (warp == kLoadWarp) {
         // -------------------------------------------------------------- load --
         const bool leader = elect_one();
-        float g[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};   // tokens 2 lane, 2 lane + 1 of the next chunk
-        auto fetch = [&](int c) {
-            const int m = len_of(c);
+        int kq_loaded = 0, v_loaded = 0, start = 0;
+        float g[2], be[2];           // tokens 2 lane, 2 lane + 1 from `at`
+        int at = -1;
+        auto fetch = [&](int from) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int t = 2 * lane + u;
-                const size_t at = (size_t)(tbeg + begin_of(c) + t) * a.H + h;
-                g[u] = t < m ? a.g[at] : 0.f;
-                be[u] = t < m ? a.beta[at] : 0.f;
+                const int t = from + 2 * lane + u;
+                const size_t x = (size_t)(tbeg + t) * a.H + h;
+                g[u] = t < len ? a.g[x] : 0.f;
+                be[u] = t < len ? a.beta[x] : 0.f;
+            }
+            at = from;
+        };
+        // The tiles of tokens t0 .. t0 + 63 into L2, two chunks ahead of their loads.
+        auto prefetch = [&](int t) {
+            if (!leader || t >= len) return;
+            for (int x = 0; x < kD; x += 64) {
+                tma_prefetch(&tm_k, x, hk, tbeg + t);
+                tma_prefetch(&tm_q, x, hk, tbeg + t);
+                tma_prefetch(&tm_v, x, h, tbeg + t);
             }
         };
         fetch(0);
-        int kq_loaded = 0, v_loaded = 0;
-        for (int c = 0; c < nch; ++c) {
-            const int s = c % kKQStages;
+        prefetch(kC);
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; ok && start < len; ++c) {
+            const int s = c % kKQStages, t0 = tbeg + start;
             if (c >= kKQStages && !wait(&bars.kq_empty[s], c / kKQStages - 1)) break;
-            const int t0 = tbeg + begin_of(c);
             if (leader) {
                 uint8_t *st = sm + s * kKQStage;
                 mbar_arrive_expect_tx(&bars.kq_full[s], kKQStage);
@@ -788,44 +812,61 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             ++v_loaded;
             __syncwarp();
-            // Decay tables: two tokens per lane, an inclusive scan over the warp.
-            float x[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) x[u] = (g[u] < kGClampSoftplus ? kGClampSoftplus : g[u]) * kLog2e;
-            const float pair = x[0] + x[1];
-            float sum = pair;
+            prefetch(start + 2 * kC);
+            // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row,
+            // and the range of e^{-G}; then the factors.
+            if (at != start) fetch(start);
+            int m = min(kC, len - start);
+            if (a.block > 0) m = min(m, a.block - (int)(((int64_t)ctx + start) % a.block));
+            const float x0 = g[0] * kLog2e, x1 = g[1] * kLog2e;
+            const float first = __shfl_sync(0xffffffffu, x0, 0);   // applied to the incoming state
+            const float own = lane == 0 ? x1 : x0 + x1;
+            float sum = own;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const float y = __shfl_up_sync(0xffffffffu, sum, d);
                 if (lane >= d) sum += y;
             }
-            const float tile_end = __shfl_sync(0xffffffffu, sum, lane | 7);
-            const float GC = __shfl_sync(0xffffffffu, sum, 31);
-            const float G0 = sum - x[1], G1 = sum;
-            Gate &gt = gates[s];
-            const float e0 = ex2(G0), e1 = ex2(G1);
-            *(float2 *)&gt.G[2 * lane] = make_float2(G0, G1);
-            *(float2 *)&gt.f[2 * lane] = make_float2(ex2(tile_end - G0), ex2(tile_end - G1));
-            *(float2 *)&gt.eG[2 * lane] = make_float2(e0, e1);
-            *(float2 *)&gt.beta[2 * lane] = make_float2(be[0], be[1]);
-            *(float2 *)&gt.nbe[2 * lane] = make_float2(-be[0] * e0, -be[1] * e1);
-            *(float2 *)&gt.tail[2 * lane] = make_float2(ex2(GC - G0), ex2(GC - G1));
-            // Factored decays need every tile's range inside the fp32 exponent.
-            const float tile_begin = __shfl_sync(0xffffffffu, G0, lane & 24);
-            const bool steep = __any_sync(0xffffffffu, !(tile_begin - tile_end <= 100.f) || x[0] > 0.f || x[1] > 0.f);
-            if (lane == 0) { gt.eGC = ex2(GC); gt.steep = steep; }
+            const float before = __shfl_up_sync(0xffffffffu, sum, 1);
+            const float G0 = lane == 0 ? 0.f : before + x0, G1 = sum;
+            // (A positive log-decay: G need not fall, so it stays within kSafe either way.)
+            const float range = __any_sync(0xffffffffu, x0 > 0.f || x1 > 0.f) ? kSafe : kRange;
+            const uint32_t out0 = __ballot_sync(0xffffffffu, !(fabsf(G0) <= range));
+            const uint32_t out1 = __ballot_sync(0xffffffffu, !(fabsf(G1) <= range));
+            if (out0) m = min(m, 2 * (__ffs(out0) - 1));
+            if (out1) m = min(m, 2 * (__ffs(out1) - 1) + 1);
+            const float GC = __shfl_sync(0xffffffffu, (m - 1) & 1 ? G1 : G0, (m - 1) >> 1);
+            const float shift = fmaxf(0.f, -GC - kSafe);
+            const bool in0 = 2 * lane < m, in1 = 2 * lane + 1 < m;
+            Info &in = infos[c % kInfos];
+            *(float2 *)&in.beta[2 * lane] = make_float2(in0 ? be[0] : 0.f, in1 ? be[1] : 0.f);
+            *(float2 *)&in.ev[2 * lane] = make_float2(in0 ? be[0] * ex2(-G0 - shift) : 0.f,
+                                                      in1 ? be[1] * ex2(-G1 - shift) : 0.f);
+            *(float2 *)&in.eo[2 * lane] = make_float2(in0 ? a.scale * ex2(G0 + shift) : 0.f,
+                                                      in1 ? a.scale * ex2(G1 + shift) : 0.f);
+            if (lane == 0) {
+                in.in = ex2(first - shift);
+                in.out = ex2(GC + shift);
+                in.start = start;
+                in.len = m;
+                in.last = start + m >= len;
+            }
             __syncwarp();
-            if (leader) mbar_arrive(&bars.gate_full[s]);
-            if (c + 1 < nch) fetch(c + 1);
+            if (leader) mbar_arrive(&bars.info_full[c % kInfos]);
+            start += m;
+            if (start < len) fetch(start);
         }
         // Every tile has landed before the CTA may exit.
         if (leader) {
+#pragma unroll 1
             for (int c = max(0, kq_loaded - kKQStages); c < kq_loaded; ++c)
-                mbar_wait(&bars.kq_full[c % kKQStages], (c / kKQStages) & 1, globaltimer_ns() + kWaitNs);
+                mbar_wait(&bars.kq_full[c % kKQStages], (c / kKQStages) & 1, globaltimer_ns() + kDrainNs);
+#pragma unroll 1
             for (int c = max(0, v_loaded - kVStages); c < v_loaded; ++c)
-                mbar_wait(&bars.v_full[c % kVStages], (c / kVStages) & 1, globaltimer_ns() + kWaitNs);
+                mbar_wait(&bars.v_full[c % kVStages], (c / kVStages) & 1, globaltimer_ns() + kDrainNs);
         }
         __syncwarp();
+    }
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -846,7 +887,7 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream)
     mk = mv = mo = mq;   // with no tokens no tile is read or written
     if (a.total_tokens > 0 &&
         (!tc_rows_map(&mq, a.q, a.total_tokens, a.Hk) || !tc_rows_map(&mk, a.k, a.total_tokens, a.Hk) ||
-         !tc_rows_map(&mv, a.v, a.total_tokens, a.H) || !tc_out_map(&mo, a.o, a.total_tokens, a.H, 32)))
+         !tc_rows_map(&mv, a.v, a.total_tokens, a.H) || !tc_out_map32(&mo, a.o, a.total_tokens, a.H)))
         return cudaErrorInvalidValue;
     // Longest sequences first (they set the end of the launch); the host offsets only
     // order the CTAs, each of which reads its own bounds on the device.

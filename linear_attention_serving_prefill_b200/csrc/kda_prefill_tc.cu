@@ -1712,7 +1712,8 @@ bool encode_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H)
 // o [T][H][128] bf16 as a 3-D tensor (channel, head, token) with a {128, 1, 64}
 // box and no swizzle: one chunk's output rows of one head per TMA store, from
 // a dense [64][128] staging tile.
-bool encode_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t channels = kDV)
+bool encode_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t channels = kDV,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE)
 {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
@@ -1721,7 +1722,7 @@ bool encode_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t
     const cuuint32_t box[3] = {(cuuint32_t)channels, 1, (cuuint32_t)kChunk};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1732,9 +1733,9 @@ bool tc_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H)
     return encode_rows_map(map, base, T, H);
 }
 
-bool tc_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t channels)
+bool tc_out_map32(CUtensorMap *map, void *base, int32_t T, int32_t H)
 {
-    return encode_out_map(map, base, T, H, channels);
+    return encode_out_map(map, base, T, H, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 namespace {
