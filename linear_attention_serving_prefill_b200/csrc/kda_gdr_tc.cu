@@ -65,18 +65,18 @@ constexpr int kThreads = 24 * 32;             // whole warpgroups (one warp idle
 // [k K0 | q K0 | k K1 | q K1], 8 KiB each (64 rows x 128 B, 128-byte swizzle): the
 // 128-row operand [K; Q] per half of 64 channels.  V: two halves of 8 KiB.
 constexpr uint32_t kKQStage = 32768, kVStage = 16384;
-constexpr int kKQStages = 3, kVStages = 2, kInfos = 8;
+constexpr int kKQStages = 3, kVStages = 2, kInfos = 8, kPBufs = 3;
 constexpr uint32_t kOffV = kKQStages * kKQStage;
 constexpr uint32_t kOffW = kOffV + kVStages * kVStage;   // W^T: 128 channels x 64 tokens
-constexpr uint32_t kOffP = kOffW + 16384;                // P: 64 x 64, two buffers
-constexpr uint32_t kOffT1 = kOffP + 2 * 8192;            // -T Diag(beta): 64 x 64
+constexpr uint32_t kOffP = kOffW + 16384;                // P: 64 x 64, three buffers
+constexpr uint32_t kOffT1 = kOffP + kPBufs * 8192;            // -T Diag(beta): 64 x 64
 constexpr uint32_t kOffT2 = kOffT1 + 8192;               // T Diag(beta e^{-G})
 constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group: fp32 blocks, see kMBlock
 // A's 32 x 32 diagonal blocks (then T's) and its lower-left block, rows padded to 36.
 constexpr int kLd = 36, kMBlock = 32 * kLd;
 constexpr uint32_t kMGroup = 3 * kMBlock * 4;
-constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 4 KiB a warp
-constexpr uint32_t kSmem = kOffO + 4 * 4096 + 1024;
+constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 2 KiB a warp
+constexpr uint32_t kSmem = kOffO + 4 * 2048 + 1024;
 
 // TMEM columns.
 constexpr uint32_t kTS = 0;      // S^T, fp32 [dv][dk]
@@ -90,22 +90,24 @@ constexpr uint32_t kTW = 448;    // W^T accumulator [dk][token]
 struct Bars {
     uint64_t kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos];
     uint64_t v_full[kVStages], v_empty[kVStages];   // v_empty: the product with V and T is done
-    uint64_t ap_full[2], o_full[2], w_full[2], zeroed[2];
+    uint64_t ap_full[2], o_full[kPBufs], w_full[2], zeroed[2];
     uint64_t ap_tfree, t_ready, w_tfree, w_ready;
     uint64_t s_ready, f_ready, f_full, s_full, o_free;
     uint64_t drain[2];
 };
 
-// Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks; the load warp
-// writes chunk c + 2's only when the product with V of chunk c is done, which is behind every
-// read of chunk c - 3's.
+// Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks: the load warp
+// writes chunk c's once the state product of chunk c - 4 is done, and every read of chunk
+// c - 8's comes before the products of chunk c - 6.
 struct __align__(16) Info {
     float beta[kC];   // 0 past the chunk's last token
     float ev[kC];     // beta e^{-G}
     float eo[kC];     // scale e^{G}
     float in, out;    // factors of the state: before the chunk (first token's e^g), after it (e^{G_C})
     int start, len;   // first token in the sequence, tokens
-    int last, pad[3];
+    int last;         // the sequence ends with this chunk
+    int row;          // pool row of a block that ends with it, or -1
+    int pad[2];
 };
 
 struct Params {
@@ -185,57 +187,68 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *sm
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t0), "r"(smem_u32(smem_src))
                  : "memory");
 }
-__device__ __forceinline__ void named_timeout(int32_t *status) {
-    atomicCAS(status, 0, (int32_t)KDA_TC_TIMEOUT_CODE);
+__device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
 }
 
-// Off-diagonal block of the inverse of a lower-triangular matrix from its inverted diagonal
-// blocks: Z = (T_ii A_ij) T_jj (the caller negates), all blocks W x W with leading dimension
-// kLd.  T's blocks are stored rounded to tf32, A too unless ROUND_A (T goes on to bf16, eight
-// times coarser).  This warp forms the 16 rows from rr, of them NT 8-column tiles from column n0.
-template <int W, int NT, bool ROUND_A>
-__device__ __forceinline__ void block_product(const float *Ti, const float *A, const float *Tj, int rr, int n0,
-                                              int lane, float (&z)[NT][4]) {
+// Off-diagonal block of the inverse of a lower-triangular matrix, transposed: Z^T = (T_jj^T
+// A_ij^T) T_ii^T (the caller negates), W x W blocks with leading dimension kLd, T's blocks
+// stored transposed, everything rounded to tf32 where it was stored (T goes on to bf16, eight
+// times coarser).  This warp forms rows j0 .. j0 + 15 (columns of the block) and, of them,
+// columns i0 .. i0 + 15 (rows of the block).
+template <int W>
+__device__ __forceinline__ void block_product(const float *TjT, const float *A, const float *TiT, int j0, int i0,
+                                              int lane, float (&z)[2][4]) {
     const int g = lane >> 2, t = lane & 3;
-    float y[W / 8][4];
+    float v[W / 8][4];
 #pragma unroll
-    for (int n = 0; n < W / 8; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
+    for (int n = 0; n < W / 8; ++n) v[n][0] = v[n][1] = v[n][2] = v[n][3] = 0.f;
+    // 32-bit tiles through the 16-bit matrix load: a row of 16 bytes is four values.
+    const uint32_t pa = smem_u32(TjT + (j0 + (lane & 15)) * kLd + (lane >> 4) * 4);
+    const uint32_t pb = smem_u32(A + (lane & 7) * kLd + (lane >> 3) * 4);
 #pragma unroll 1
-    for (int k = 0; k < rr + 16; k += 8) {    // T_ii is lower triangular
-        const float *p = Ti + (rr + g) * kLd + k + t, *q = A + (k + t) * kLd + g;
-        const uint32_t a[4] = {__float_as_uint(p[0]), __float_as_uint(p[8 * kLd]), __float_as_uint(p[4]),
-                               __float_as_uint(p[8 * kLd + 4])};
+    for (int k = j0; k < W; k += 16) {     // T_jj^T is upper triangular
+        uint32_t a0[4], a1[4];
+        ldmatrix4(pa + 4 * k, a0);
+        ldmatrix4(pa + 4 * k + 32, a1);
 #pragma unroll
         for (int n = 0; n < W / 8; ++n) {
-            const float b0 = q[8 * n], b1 = q[4 * kLd + 8 * n];
-            mma_tf32(y[n], a, ROUND_A ? tf32(b0) : __float_as_uint(b0), ROUND_A ? tf32(b1) : __float_as_uint(b1));
+            uint32_t b[4];
+            ldmatrix4(pb + 4 * (8 * n * kLd + k), b);
+            mma_tf32(v[n], a0, b[0], b[1]);
+            mma_tf32(v[n], a1, b[2], b[3]);
         }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
-    // Y's accumulators are the A operand with the contraction index permuted: slot t is
+    for (int n = 0; n < 2; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
+    // The accumulators are the A operand with the contraction index permuted: slot t is
     // column 2t, slot t + 4 is column 2t + 1; B reads its rows in the same order.
 #pragma unroll
     for (int k = 0; k < W / 8; ++k) {
-        const uint32_t a[4] = {tf32(y[k][0]), tf32(y[k][2]), tf32(y[k][1]), tf32(y[k][3])};
-        const float *q = Tj + (8 * k + 2 * t) * kLd + n0 + g;
+        if (8 * k > i0 + 15) break;        // T_ii is lower triangular
+        const uint32_t a[4] = {tf32(v[k][0]), tf32(v[k][2]), tf32(v[k][1]), tf32(v[k][3])};
+        const float *q = TiT + (8 * k + 2 * t) * kLd + i0 + g;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (8 * k + 7 >= n0 + 8 * n)
-                mma_tf32(z[n], a, __float_as_uint(q[8 * n]), __float_as_uint(q[kLd + 8 * n]));
+        for (int n = 0; n < 2; ++n)
+            mma_tf32(z[n], a, __float_as_uint(q[8 * n]), __float_as_uint(q[kLd + 8 * n]));
     }
 }
 
-// The rest of a wait whose first try did not succeed.  Not inlined: there are forty waits, and
-// the roles' code has to stay in the instruction cache together.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t *status) {
-    uint64_t *p = (uint64_t *)__cvta_shared_to_generic(bar);
-    bool r = false;
-#pragma unroll 1
-    for (uint32_t i = 0; i < kTries && !r; ++i)
-        r = __all_sync(0xffffffffu, mbar_try_wait_hint(p, parity, kSuspendNs));
-    if (!r) named_timeout(status);
-    return r;
+// Waits until the phase with the given parity completes, for kTries tries at most, in a loop
+// of a few instructions (there are forty waits, and the roles' code has to stay in the
+// instruction cache together).
+__device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, %3;\n"
+        "TRY%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n @p bra DONE%=;\n"
+        " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra TRY%=;\n"
+        "DONE%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kTries), "n"(kSuspendNs)
+        : "memory");
+    return ok != 0;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -274,13 +287,13 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int s = 0; s < kKQStages; ++s) {
             mbar_init(&bars.kq_full[s], 1);
             mbar_init(&bars.kq_empty[s], 1);
+            mbar_init(&bars.o_full[s], 1);
         }
         for (int s = 0; s < kInfos; ++s) mbar_init(&bars.info_full[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
             mbar_init(&bars.ap_full[s], 1);
-            mbar_init(&bars.o_full[s], 1);
             mbar_init(&bars.w_full[s], 1);
             mbar_init(&bars.zeroed[s], kGroupThreads);
             mbar_init(&bars.drain[s], 1);
@@ -297,8 +310,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         fence_mbar_init();
     }
     // The upper right quadrants of P and T's operands are zero in every chunk.
-    for (int e = tid; e < 4 * 32 * 4; e += kThreads) {
-        const uint32_t img = e < 256 ? kOffP + (e >> 7) * 8192 : (e < 384 ? kOffT1 : kOffT2);
+    for (int e = tid; e < (kPBufs + 2) * 128; e += kThreads) {
+        const uint32_t img = kOffP + (e >> 7) * 8192;   // P's buffers, then T's operands
         *(uint4 *)(sm + img + sw128_offset((e >> 2) & 31, 32 + 8 * (e & 3), 64)) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
@@ -309,13 +322,21 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t tb = tbase;
     const uint32_t lq = 32 * (warp & 3);   // this warp's TMEM lanes
 
-    // Bounded wait of a whole warp; on expiry the timeout is recorded and the role leaves its
-    // loop (the others run into the same limit).
+    // Bounded wait of a whole warp; once one has given up every later one fails at once, the
+    // role leaves its loop and the timeout is recorded at the end (the other roles run into
+    // the same limit).
+    bool alive = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity & 1, kSuspendNs))) return true;
-        return wait_slow(smem_u32(bar), parity & 1, a.status);
+        alive = alive && __all_sync(0xffffffffu, try_phase(bar, parity & 1));
+        return alive;
     };
     auto wait_info = [&](int c) { return wait(&bars.info_full[c % kInfos], c / kInfos); };
+    // Stage and phase of chunk c in the K/Q ring, advanced chunk by chunk.
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&] {
+        if (++stage == kKQStages) { stage = 0; phase ^= 1; }
+    };
 
     if (warp < kIntraWarp) {
         // ------------------------------------------------------------- chain --
@@ -343,7 +364,6 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const Info &in = infos[c % kInfos];
             const bool last = in.last != 0;
             const float out = in.out;
-            const int64_t done = (int64_t)ctx + in.start + in.len;
             // F^T of this half's 32 tokens -> bf16.
             ok = wait(&bars.f_full, c);
             if (!ok) break;
@@ -356,43 +376,41 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_st_wait();
             tc_fence_before_sync();
             mbar_arrive(&bars.f_ready);
-            // Rows that keep the state after this chunk: a block that ends here, the last state.
-            int row = -1;
-            if (a.block > 0 && done % a.block == 0 && done / a.block <= a.table_cols)
-                row = a.table[(size_t)n * a.table_cols + done / a.block - 1];
-            if (row >= a.pool_size) row = -1;
+            const int row = in.row;
             if (!last) ok = wait_info(c + 1);
             const float f = last ? 0.f : out * infos[(c + 1) % kInfos].in;
             ok = ok && wait(&bars.s_full, c);
             if (!ok) break;
             tc_fence_after_sync();
+            if (row >= 0 || last) {   // rows that keep the state after this chunk
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) {
+                    const int to = w < 2 ? row : (last ? dst : -1), p = w & 1;
+                    if (to < 0) continue;
+                    tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
+                    tmem_ld_wait();
+                    float *Sf = row_of(to) + (size_t)(64 * hh + 32 * p) * kD + j;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) Sf[(size_t)i * kD] = __uint_as_float(x[i]) * out;
+                }
+                if (last) break;
+            }
 #pragma unroll 1
             for (int p = 0; p < 2; ++p) {
                 tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
                 tmem_ld_wait();
-                if (row >= 0 || last) {
-#pragma unroll 1
-                    for (int w = 0; w < 2; ++w) {
-                        const int to = w == 0 ? row : (last ? dst : -1);
-                        if (to < 0) continue;
-                        float *Sf = row_of(to) + (size_t)(64 * hh + 32 * p) * kD + j;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) Sf[(size_t)i * kD] = __uint_as_float(x[i]) * out;
-                    }
-                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 v = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                    const float2 t = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
                                                 make_float2(f, f));
-                    x[2 * i] = __float_as_uint(v.x);
-                    x[2 * i + 1] = __float_as_uint(v.y);
-                    y[i] = pack(v.x, v.y);
+                    x[2 * i] = __float_as_uint(t.x);
+                    x[2 * i + 1] = __float_as_uint(t.y);
+                    y[i] = pack(t.x, t.y);
                 }
                 tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh + 16 * p), y);
                 tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
             }
             tmem_st_wait();
-            if (last) break;
             tc_fence_before_sync();
             mbar_arrive(&bars.s_ready);
         }
@@ -403,7 +421,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool is_p = wq >= 2;
         float *D0 = (float *)(sm + kOffM + group * kMGroup), *D1 = D0 + kMBlock, *X = D1 + kMBlock;
         bool ok = true;
-        if (group == 1) ok = wait_info(0);
+        if (group == 1) { ok = wait_info(0); next_stage(); }
         bool more = group == 0 || (ok && !infos[0].last);
 #pragma unroll 1
         for (int c = group; more; c += 2) {
@@ -412,9 +430,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (in.len < kC) {
                 // Rows past the last token (another sequence's, or unwritten ones) become zeros
                 // in K and V, before any product reads the tiles.
-                ok = ok && wait(&bars.kq_full[c % kKQStages], c / kKQStages) &&
-                     wait(&bars.v_full[c % kVStages], c / kVStages);
-                uint8_t *kt = sm + (c % kKQStages) * kKQStage, *vt = sm + kOffV + (c % kVStages) * kVStage;
+                ok = ok && wait(&bars.kq_full[stage], phase) && wait(&bars.v_full[c % kVStages], c / kVStages);
+                uint8_t *kt = sm + stage * kKQStage, *vt = sm + kOffV + (c % kVStages) * kVStage;
 #pragma unroll 1
                 for (int e = it; e < (kC - in.len) * 8; e += kGroupThreads) {
                     const uint32_t at = (uint32_t)(in.len + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
@@ -427,60 +444,41 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 fence_proxy_async_smem();
                 mbar_arrive(&bars.zeroed[group]);
             }
-            // This group's blocks: every thread has read chunk c - 2's.
+            // This group's blocks (every thread has read chunk c - 2's) and P's buffer (read by
+            // the outputs of chunk c - 3).
             if (c >= 2) ok = ok && wait(&bars.w_full[c & 1], (c >> 1) - 1);
+            if (c >= kPBufs) ok = ok && wait(&bars.o_full[stage], phase ^ 1);
             const float br = in.beta[r];
             ok = ok && wait(&bars.ap_full[c & 1], c >> 1);
             tc_fence_after_sync();
-            uint32_t near[16], far[16];    // P's row, packed (A goes straight to its blocks)
-            {                              // columns 32 half .. + 31, up to the diagonal
-                uint32_t v[32];
-                tmem_ld32(tmem_addr(tb, lq, kTAP + 32 * half), v);
+            // Columns 0 .. 32 half + 31 of this row, a 16-token tile at a time: A to its blocks in
+            // fp32, P to its operand.
+            uint8_t *img = sm + kOffP + stage * 8192;
+#pragma unroll 1
+            for (int s0 = 0; s0 < 32 * (1 + half); s0 += 16) {
+                const int lim = (is_p ? r : r - 1) - s0;    // last column kept (15 or more: all)
+                float v[16];
+                tmem_ld16f(tmem_addr(tb, lq, kTAP + s0), v);
                 tmem_ld_wait();
-                const int lim = (is_p ? r : r - 1) - 32 * half;   // last column kept
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = i <= lim ? v[i] : 0.f;
                 if (is_p) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = i <= lim ? v[i] : 0u;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) near[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    for (int i = 0; i < 16; i += 8)
+                        *(uint4 *)(img + sw128_offset(r, s0 + i, 64)) =
+                            make_uint4(pack(v[i], v[i + 1]), pack(v[i + 2], v[i + 3]), pack(v[i + 4], v[i + 5]),
+                                       pack(v[i + 6], v[i + 7]));
                 } else {
-                    float *m = (half ? D1 : D0) + (r & 31) * kLd;
+                    float *m = (!half ? D0 : (s0 < 32 ? X : D1)) + (r & 31) * kLd + (s0 & 31);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = i <= lim ? __float_as_uint(__uint_as_float(v[i]) * br) : 0u;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) *(uint4 *)&m[i] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    for (int i = 0; i < 16; i += 4)
+                        *(uint4 *)&m[i] = make_uint4(tf32(v[i] * br), tf32(v[i + 1] * br), tf32(v[i + 2] * br), tf32(v[i + 3] * br));
                 }
             }
-            if (half) {                    // columns 0-31 of rows 32-63
-                uint32_t v[32];
-                tmem_ld32(tmem_addr(tb, lq, kTAP), v);
-                tmem_ld_wait();
-                if (is_p) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) far[i] = pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                } else {
-                    float *m = X + (r & 31) * kLd;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *(uint4 *)&m[i] = make_uint4(tf32(__uint_as_float(v[i]) * br), tf32(__uint_as_float(v[i + 1]) * br),
-                                                     tf32(__uint_as_float(v[i + 2]) * br), tf32(__uint_as_float(v[i + 3]) * br));
-                }
-            }
+            if (is_p) fence_proxy_async_smem();
             tc_fence_before_sync();
             mbar_arrive(&bars.ap_tfree);
             if (group_sync_any(group, !ok)) break;
-            if (is_p) {   // P's buffer: read by the outputs of chunk c - 2
-                if (c >= 2) ok = ok && wait(&bars.o_full[c & 1], (c >> 1) - 1);
-                uint8_t *img = sm + kOffP + (c & 1) * 8192;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    *(uint4 *)(img + sw128_offset(r, 32 * half + 8 * i, 64)) =
-                        make_uint4(near[4 * i], near[4 * i + 1], near[4 * i + 2], near[4 * i + 3]);
-                    if (half)
-                        *(uint4 *)(img + sw128_offset(r, 8 * i, 64)) =
-                            make_uint4(far[4 * i], far[4 * i + 1], far[4 * i + 2], far[4 * i + 3]);
-                }
-            }
             // Inverse of the two 32 x 32 diagonal blocks, one warp each: half a warp solves a
             // 16 x 16 block, lane j its column j, four unknowns at a time; then the block
             // between them.
@@ -504,14 +502,14 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) B[i * kLd + j] = __uint_as_float(tf32(x[i]));
+                for (int i = 0; i < 16; i += 4)   // transposed: lane j's column is row j
+                    *(uint4 *)&B[j * kLd + i] = make_uint4(tf32(x[i]), tf32(x[i + 1]), tf32(x[i + 2]), tf32(x[i + 3]));
                 __syncwarp();
                 float z[2][4];
-                block_product<16, 2, true>(Dw + 16 * (kLd + 1), Dw + 16 * kLd, Dw, 0, 0, lane, z);
-                __syncwarp();
+                block_product<16>(Dw, Dw + 16 * kLd, Dw + 16 * (kLd + 1), 0, 0, lane, z);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float *p = Dw + (16 + g) * kLd + 8 * q + 2 * t;
+                    uint32_t *p = (uint32_t *)&Dw[g * kLd + 16 + 8 * q + 2 * t];
                     *(uint2 *)p = make_uint2(tf32(-z[q][0]), tf32(-z[q][1]));
                     *(uint2 *)(p + 8 * kLd) = make_uint2(tf32(-z[q][2]), tf32(-z[q][3]));
                 }
@@ -522,36 +520,40 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ok = ok && wait(&bars.v_empty[(c - 1) & 1], (c - 1) >> 1);
             }
             if (group_sync_any(group, !ok)) break;
-            {   // rows 32-63, columns 0-31: 16 x 16 per warp, straight to the operands
-                const int rr = 16 * half, nc = 16 * (wq >> 1), g = lane >> 2, t = lane & 3;
+            // T's two operands, rows i, columns j: tiles of T^T times the column's factor, stored
+            // transposed.
+            const int g = lane >> 2, t = lane & 3;
+            {   // rows 32-63, columns 0-31: 16 x 16 per warp
+                const int i0 = 16 * half, j0 = 16 * (wq >> 1);
                 float z[2][4];
-                block_product<32, 2, false>(D1, X, D0, rr, nc, lane, z);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int col = nc + 8 * q + 2 * t;
-                    const float2 be = *(const float2 *)&in.beta[col], ev = *(const float2 *)&in.ev[col];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t at = sw128_offset(32 + rr + g + 8 * u, col, 64);
-                        *(uint32_t *)(sm + kOffT1 + at) = pack(z[q][2 * u] * be.x, z[q][2 * u + 1] * be.y);
-                        *(uint32_t *)(sm + kOffT2 + at) = pack(-z[q][2 * u] * ev.x, -z[q][2 * u + 1] * ev.y);
-                    }
-                }
+                block_product<32>(D0, X, D1, j0, i0, lane, z);
+                const uint32_t at = sw128_offset(32 + i0 + 8 * (lane >> 4) + (lane & 7), j0 + 8 * ((lane >> 3) & 1), 64);
+                const float be0 = in.beta[j0 + g], be1 = in.beta[j0 + g + 8];
+                const float ev0 = -in.ev[j0 + g], ev1 = -in.ev[j0 + g + 8];
+                stmatrix4_trans(smem_u32(sm + kOffT1) + at, pack(z[0][0] * be0, z[0][1] * be0), pack(z[0][2] * be1, z[0][3] * be1),
+                                pack(z[1][0] * be0, z[1][1] * be0), pack(z[1][2] * be1, z[1][3] * be1));
+                stmatrix4_trans(smem_u32(sm + kOffT2) + at, pack(z[0][0] * ev0, z[0][1] * ev0), pack(z[0][2] * ev1, z[0][3] * ev1),
+                                pack(z[1][0] * ev0, z[1][1] * ev0), pack(z[1][2] * ev1, z[1][3] * ev1));
             }
-            {   // the diagonal blocks: half of the threads per operand, a row each
-                const float *m = (r < 32 ? D0 : D1) + (r & 31) * kLd;
-                const float *colf = (is_p ? in.ev : in.beta) + (r & 32);
-                const float sign = is_p ? 1.f : -1.f;
-                uint8_t *to = sm + (is_p ? kOffT2 : kOffT1);
+            {   // the diagonal blocks: a block and an operand per warp, eight rows at a time
+                const float *Dw = half ? D1 : D0;
+                const uint32_t img = smem_u32(sm + (is_p ? kOffT2 : kOffT1));
+                float fac[4];
 #pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int col = 32 * half + 8 * m + g;
+                    fac[m] = is_p ? in.ev[col] : -in.beta[col];
+                }
+#pragma unroll 1
                 for (int i = 0; i < 32; i += 8) {
-                    const float4 x = *(const float4 *)&m[i], y = *(const float4 *)&m[i + 4];
-                    float4 p = *(const float4 *)&colf[i], q = *(const float4 *)&colf[i + 4];
-                    p.x *= sign; p.y *= sign; p.z *= sign; p.w *= sign;
-                    q.x *= sign; q.y *= sign; q.z *= sign; q.w *= sign;
-                    *(uint4 *)(to + sw128_offset(r, (r & 32) + i, 64)) =
-                        make_uint4(pack(x.x * p.x, x.y * p.y), pack(x.z * p.z, x.w * p.w),
-                                   pack(y.x * q.x, y.y * q.y), pack(y.z * q.z, y.w * q.w));
+                    uint32_t p[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const float2 x = *(const float2 *)&Dw[(8 * m + g) * kLd + i + 2 * t];
+                        p[m] = 8 * m <= i ? pack(x.x * fac[m], x.y * fac[m]) : 0u;
+                    }
+                    stmatrix4_trans(img + sw128_offset(32 * half + i + (lane & 7), 32 * half + 8 * (lane >> 3), 64),
+                                    p[0], p[1], p[2], p[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -561,47 +563,56 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ok = ok && wait_info(c + 1);
                 more = ok && !infos[(c + 1) % kInfos].last;
             }
+            next_stage();
+            next_stage();
         }
     } else if (warp < kIssueWarp) {
         // --------------------------------------------------------------- aux --
         const int wq = warp & 3, it = 32 * wq + lane;
-        uint8_t *ost = sm + kOffO + 4096 * wq;     // [64 tokens][32 channels] of this warp
+        uint8_t *ost = sm + kOffO + 2048 * wq;     // two tiles of [16 tokens][32 channels]
         __nv_bfloat16 *o = (__nv_bfloat16 *)a.o;
         const uint32_t osa = smem_u32(ost) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
         uint32_t xa[32], xb[32];
         auto output = [&](int c) {
             const Info &in = infos[c % kInfos];
-            if (!wait(&bars.o_full[c & 1], c >> 1)) return false;
+            if (!wait(&bars.o_full[stage], phase)) return false;
+            next_stage();
             tc_fence_after_sync();
+            const int m = in.len, t0 = tbeg + in.start;
+            // 16 tokens at a time through two 1 KiB tiles: four 8 x 8 blocks (channels x tokens)
+            // become eight token rows of 32 channels, 16-byte pieces swizzled by token pair.
             tmem_ld_tiles(tmem_addr(tb, lq, kTO), xa);
             tmem_ld_tiles(tmem_addr(tb, lq + 16, kTO), xb);
             tmem_ld_wait();
             tc_fence_before_sync();
             mbar_arrive(&bars.o_free);
-            const int m = in.len, t0 = tbeg + in.start;
-            if (lane == 0) bulk_wait_read<0>();    // the previous chunk's store has read the tile
-            __syncwarp();
-            // Eight tokens at a time: four 8 x 8 tiles (channels x tokens) become eight token
-            // rows of 32 channels; 16-byte pieces swizzled by token pair against conflicts.
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 d = *(const float2 *)&in.eo[8 * j + 2 * (lane & 3)];
-                auto scaled = [&](const uint32_t *x) {
-                    return pack(__uint_as_float(x[0]) * d.x, __uint_as_float(x[1]) * d.y);
-                };
-                stmatrix4_trans(osa + j * 512, scaled(xa + 4 * j), scaled(xa + 4 * j + 2), scaled(xb + 4 * j),
-                                scaled(xb + 4 * j + 2));
-            }
-            if (m == kC) {
+            for (int q = 0; q < 4; ++q) {
+                if (16 * q >= m) break;
+                const uint32_t tile = (q & 1) * 1024;
+                if (lane == 0) bulk_wait_read<1>();    // the store before the last has read this tile
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t *u = xa + 8 * q + 4 * j, *v = xb + 8 * q + 4 * j;
+                    const float2 d = *(const float2 *)&in.eo[16 * q + 8 * j + 2 * (lane & 3)];
+                    auto scaled = [&](const uint32_t *x) {
+                        return pack(__uint_as_float(x[0]) * d.x, __uint_as_float(x[1]) * d.y);
+                    };
+                    stmatrix4_trans(osa + tile + j * 512, scaled(u), scaled(u + 2), scaled(v), scaled(v + 2));
+                }
+                if (16 * q + 16 > m) break;            // only some of these rows are the chunk's
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) { tma_store(&tm_o, ost, 32 * wq, h, t0); bulk_commit(); }
-            } else {       // a partial chunk: only its own rows
+                if (lane == 0) { tma_store(&tm_o, ost + tile, 32 * wq, h, t0 + 16 * q); bulk_commit(); }
+            }
+            if (m & 15) {
                 __syncwarp();
+                const int q = m >> 4;
 #pragma unroll 1
-                for (int e = lane; e < m * 4; e += 32)
-                    *(uint4 *)(o + ((size_t)(t0 + (e >> 2)) * a.H + h) * kD + 32 * wq + 8 * (e & 3)) =
-                        *(const uint4 *)(ost + (e >> 2) * 64 + (((e & 3) ^ ((e >> 3) & 3)) << 4));
+                for (int e = lane; e < (m & 15) * 4; e += 32)
+                    *(uint4 *)(o + ((size_t)(t0 + 16 * q + (e >> 2)) * a.H + h) * kD + 32 * wq + 8 * (e & 3)) =
+                        *(const uint4 *)(ost + (q & 1) * 1024 + (e >> 2) * 64 + (((e & 3) ^ ((e >> 3) & 3)) << 4));
                 __syncwarp();
             }
             return true;
@@ -617,13 +628,13 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ok = ok && wait(&bars.w_full[c & 1], c >> 1);
             if (!ok) break;
             tc_fence_after_sync();
+            if (c > 0) ok = wait(&bars.f_full, c - 1);   // the image: read by chunk c - 1's product
+            if (!ok) break;
             tmem_ld32(tmem_addr(tb, lq, kTW), xa);
             tmem_ld32(tmem_addr(tb, lq, kTW + 32), xb);
             tmem_ld_wait();
             tc_fence_before_sync();
             mbar_arrive(&bars.w_tfree);
-            if (c > 0) ok = wait(&bars.f_full, c - 1);   // the image: read by chunk c - 1's product
-            if (!ok) break;
             auto piece = [&](const uint32_t *x, int col) {
                 *(uint4 *)(sm + kOffW + sw128_offset(it, col, 128)) =
                     make_uint4(pack(__uint_as_float(x[0]), __uint_as_float(x[1])), pack(__uint_as_float(x[2]), __uint_as_float(x[3])),
@@ -651,11 +662,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
         for (int c = -1; ok; ++c) {
             if (c >= 0) {
-                const int s = c % kKQStages;
+                const int s = stage;
                 const uint32_t st = smem_u32(sm + s * kKQStage);
                 const uint64_t dQ = desc_kmajor_sw128(st + 8192), dK = desc_mnmajor_sw128(st, 16384);
-                const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + (c & 1) * 8192));
-                ok = wait(&bars.kq_full[s], c / kKQStages) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
+                const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + s * 8192));
+                ok = wait(&bars.kq_full[s], phase) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (leader) {   // [F^T] += S^T (-W)^T
@@ -685,10 +696,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_ts(tmem_addr(tb, 0, kTO), fb + 8 * ks, dP + ks * (32 >> 4), id64, true);
-                    mma_commit(&bars.o_full[c & 1]);
+                    mma_commit(&bars.o_full[s]);
                 }
                 __syncwarp();
                 more = !infos[c % kInfos].last;
+                next_stage();
             }
             if (!more) break;
             // [F^T] = V^T (T Diag(beta e^{-G}))^T of the next chunk.
@@ -719,8 +731,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
         for (int c = -1; ok; ++c) {   // A and P a chunk ahead of W
             if (more) {               // [AP] = [K; Q] K^T
-                const int d = c + 1, s = d % kKQStages;
-                ok = wait_info(d) && wait(&bars.kq_full[s], d / kKQStages);
+                const int d = c + 1, s = stage;
+                ok = wait_info(d) && wait(&bars.kq_full[s], phase);
                 if (ok && infos[d % kInfos].len < kC) {
                     const int g = d & 1;
                     ok = wait(&bars.zeroed[g], g ? zeros[1] : zeros[0]);
@@ -740,6 +752,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
                 more = !infos[d % kInfos].last;
+                next_stage();
             }
             if (c < 0) continue;
             ok = wait(&bars.t_ready, c) && (c == 0 || wait(&bars.w_tfree, c - 1));
@@ -765,8 +778,9 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // -------------------------------------------------------------- load --
         const bool leader = elect_one();
         int kq_loaded = 0, v_loaded = 0, start = 0;
-        float g[2], be[2];           // tokens 2 lane, 2 lane + 1 from `at`
-        int at = -1;
+        // Tokens left in the current block, and its index (no blocks: more than there are).
+        int to_block = a.block > 0 ? a.block - ctx % a.block : 0x7fffffff, blk = a.block > 0 ? ctx / a.block : 0;
+        float g[2], be[2];           // tokens 2 lane, 2 lane + 1 of the next chunk
         auto fetch = [&](int from) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -775,7 +789,6 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 g[u] = t < len ? a.g[x] : 0.f;
                 be[u] = t < len ? a.beta[x] : 0.f;
             }
-            at = from;
         };
         // The tiles of tokens t0 .. t0 + 63 into L2, two chunks ahead of their loads.
         auto prefetch = [&](int t) {
@@ -791,33 +804,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; ok && start < len; ++c) {
-            const int s = c % kKQStages, t0 = tbeg + start;
-            if (c >= kKQStages && !wait(&bars.kq_empty[s], c / kKQStages - 1)) break;
-            if (leader) {
-                uint8_t *st = sm + s * kKQStage;
-                mbar_arrive_expect_tx(&bars.kq_full[s], kKQStage);
-                tma_tile(st, &tm_k, 0, hk, t0, &bars.kq_full[s]);
-                tma_tile(st + 16384, &tm_k, 64, hk, t0, &bars.kq_full[s]);
-                tma_tile(st + 8192, &tm_q, 0, hk, t0, &bars.kq_full[s]);
-                tma_tile(st + 24576, &tm_q, 64, hk, t0, &bars.kq_full[s]);
-            }
-            ++kq_loaded;
-            __syncwarp();
-            if (c >= kVStages && !wait(&bars.v_empty[c & 1], (c >> 1) - 1)) break;
-            if (leader) {
-                uint8_t *vt = sm + kOffV + (c % kVStages) * kVStage;
-                mbar_arrive_expect_tx(&bars.v_full[c & 1], kVStage);
-                tma_tile(vt, &tm_v, 0, h, t0, &bars.v_full[c & 1]);
-                tma_tile(vt + 8192, &tm_v, 64, h, t0, &bars.v_full[c & 1]);
-            }
-            ++v_loaded;
-            __syncwarp();
-            prefetch(start + 2 * kC);
+            const int s = stage, t0 = tbeg + start;
             // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row,
             // and the range of e^{-G}; then the factors.
-            if (at != start) fetch(start);
             int m = min(kC, len - start);
-            if (a.block > 0) m = min(m, a.block - (int)(((int64_t)ctx + start) % a.block));
+            m = min(m, to_block);
             const float x0 = g[0] * kLog2e, x1 = g[1] * kLog2e;
             const float first = __shfl_sync(0xffffffffu, x0, 0);   // applied to the incoming state
             const float own = lane == 0 ? x1 : x0 + x1;
@@ -850,11 +841,40 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 in.start = start;
                 in.len = m;
                 in.last = start + m >= len;
+                in.row = -1;
+                if (m == to_block && blk < a.table_cols) {
+                    const int row = a.table[(size_t)n * a.table_cols + blk];
+                    if (row >= 0 && row < a.pool_size) in.row = row;
+                }
             }
             __syncwarp();
             if (leader) mbar_arrive(&bars.info_full[c % kInfos]);
+            if (c >= kKQStages && !wait(&bars.kq_empty[s], phase ^ 1)) break;
+            if (leader) {
+                uint8_t *st = sm + s * kKQStage;
+                mbar_arrive_expect_tx(&bars.kq_full[s], kKQStage);
+                tma_tile(st, &tm_k, 0, hk, t0, &bars.kq_full[s]);
+                tma_tile(st + 16384, &tm_k, 64, hk, t0, &bars.kq_full[s]);
+                tma_tile(st + 8192, &tm_q, 0, hk, t0, &bars.kq_full[s]);
+                tma_tile(st + 24576, &tm_q, 64, hk, t0, &bars.kq_full[s]);
+            }
+            ++kq_loaded;
+            __syncwarp();
+            if (c >= kVStages && !wait(&bars.v_empty[c & 1], (c >> 1) - 1)) break;
+            if (leader) {
+                uint8_t *vt = sm + kOffV + (c % kVStages) * kVStage;
+                mbar_arrive_expect_tx(&bars.v_full[c & 1], kVStage);
+                tma_tile(vt, &tm_v, 0, h, t0, &bars.v_full[c & 1]);
+                tma_tile(vt + 8192, &tm_v, 64, h, t0, &bars.v_full[c & 1]);
+            }
+            ++v_loaded;
+            __syncwarp();
+            prefetch(start + m + kC);
             start += m;
+            to_block -= m;
+            if (to_block == 0) { to_block = a.block; ++blk; }
             if (start < len) fetch(start);
+            next_stage();
         }
         // Every tile has landed before the CTA may exit.
         if (leader) {
@@ -868,6 +888,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
     }
     }
+    if (!alive && lane == 0) atomicCAS(a.status, 0, (int32_t)KDA_TC_TIMEOUT_CODE);
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tb, 512);

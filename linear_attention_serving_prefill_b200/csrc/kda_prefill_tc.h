@@ -31,7 +31,7 @@ size_t tc_workspace_bytes(int32_t total_tokens, int32_t num_seqs, int32_t H, int
 // and the 128-byte swizzle; false when the driver refuses it.
 bool tc_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H);
 
-// Tensor map of [T][H][128] bf16 output rows with a {32 channels, 1 head, 64 tokens}
+// Tensor map of [T][H][128] bf16 output rows with a {32 channels, 1 head, 16 tokens}
 // box and the 64-byte swizzle.
 bool tc_out_map32(CUtensorMap *map, void *base, int32_t T, int32_t H);
 
