@@ -25,17 +25,21 @@
 //   chain (warps 0-7)    F^T from its accumulator to a bf16 operand; S^T times its
 //                        factor, to the fp32 master and its bf16 copy;
 //   intra (warps 8-15)   two groups, even and odd chunks: A and P from the accumulator,
-//                        T by 16 x 16 forward substitution and two block doublings
-//                        (tf32 mma), T's two bf16 operands;
+//                        T by 16 x 16 forward substitution (fp32) and two block doublings
+//                        (fp16 warp products), T's two bf16 operands;
 //   aux   (warps 16-19)  W^T from its accumulator to a bf16 operand, O^T to o;
-//   issue (warps 20, 21) the products of the state chain; A, P and W's products;
-//   load  (warp 22)      chunk bounds and factors (a warp scan), TMA tiles.
+//   issue (warps 20, 21) the products of the state chain; W's;
+//   load  (warps 22, 23) chunk bounds and factors (a warp scan), the K and Q tiles for A and P
+//                        and their product; K, Q and V for the other products.
+// K and Q are loaded twice (the second time from L2): A and P are formed up to three chunks
+// ahead of the state, and a tile that stayed for both uses would sit idle in between.
 // Products (TMEM accumulators in brackets), chunk c:
 //   [AP] = [K; Q] K^T;  [W^T] = K^T (-T Diag(beta))^T;  [F^T] = V^T (T Diag(beta e^{-G}))^T
 //   [F^T] += S^T (-W)^T;  [O^T] = S^T Q^T;  [S^T] += F^T K;  [O^T] += F^T P^T
 // K^T, V^T and W^T are MN-major operands, so no tile is ever transposed.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cstring>
 
 #include "kda_common.cuh"
@@ -58,23 +62,27 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRange = 200.f, kSafe = 100.f;   // log2 bounds of e^{-G}, see above
 
 constexpr int kChainThreads = 256, kGroupThreads = 128, kAuxThreads = 128;
-constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kIssue2Warp = 21, kLoadWarp = 22;
-constexpr int kThreads = 24 * 32;             // whole warpgroups (one warp idles)
+constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kIssue2Warp = 21, kLoadWarp = 22, kLoad2Warp = 23;
+constexpr int kThreads = (kLoad2Warp + 1) * 32;
 
 // Shared memory (offsets from a 1024-aligned base).  A K/Q stage is
 // [k K0 | q K0 | k K1 | q K1], 8 KiB each (64 rows x 128 B, 128-byte swizzle): the
 // 128-row operand [K; Q] per half of 64 channels.  V: two halves of 8 KiB.
 constexpr uint32_t kKQStage = 32768, kVStage = 16384;
-constexpr int kKQStages = 3, kVStages = 2, kInfos = 8, kPBufs = 3;
-constexpr uint32_t kOffV = kKQStages * kKQStage;
+constexpr int kKQStages = 2, kVStages = 2, kInfos = 8, kPBufs = 3;
+constexpr uint32_t kOffEarly = kKQStages * kKQStage;     // the K/Q tile for A and P
+constexpr uint32_t kOffV = kOffEarly + kKQStage;
 constexpr uint32_t kOffW = kOffV + kVStages * kVStage;   // W^T: 128 channels x 64 tokens
 constexpr uint32_t kOffP = kOffW + 16384;                // P: 64 x 64, three buffers
 constexpr uint32_t kOffT1 = kOffP + kPBufs * 8192;            // -T Diag(beta): 64 x 64
 constexpr uint32_t kOffT2 = kOffT1 + 8192;               // T Diag(beta e^{-G})
-constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group: fp32 blocks, see kMBlock
-// A's 32 x 32 diagonal blocks (then T's) and its lower-left block, rows padded to 36.
-constexpr int kLd = 36, kMBlock = 32 * kLd;
-constexpr uint32_t kMGroup = 3 * kMBlock * 4;
+constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group, see below
+// A's four 16 x 16 diagonal blocks in fp32 (rows padded to 20); the two 32 x 32 diagonal blocks
+// of T, transposed, in fp16 (rows padded to 40; A's own block between two diagonal ones sits in
+// the unused lower left); A's rows 32-63, columns 0-31 in fp16.
+constexpr int kLdB = 20, kLdT = 40;
+constexpr uint32_t kMDiag = 16 * kLdB * 4, kMTT = 32 * kLdT * 2;
+constexpr uint32_t kMGroup = 4 * kMDiag + 3 * kMTT;
 constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 2 KiB a warp
 constexpr uint32_t kSmem = kOffO + 4 * 2048 + 1024;
 
@@ -88,17 +96,17 @@ constexpr uint32_t kTAP = 384;   // A and P accumulators (rows 0-63, 64-127)
 constexpr uint32_t kTW = 448;    // W^T accumulator [dk][token]
 
 struct Bars {
-    uint64_t kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos];
+    uint64_t early_full, kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos];
     uint64_t v_full[kVStages], v_empty[kVStages];   // v_empty: the product with V and T is done
-    uint64_t ap_full[2], o_full[kPBufs], w_full[2], zeroed[2];
+    uint64_t ap_full[2], o_full[kPBufs], w_full[2];
     uint64_t ap_tfree, t_ready, w_tfree, w_ready;
     uint64_t s_ready, f_ready, f_full, s_full, o_free;
-    uint64_t drain[2];
+    uint64_t drain[3];
 };
 
-// Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks: the load warp
-// writes chunk c's once the state product of chunk c - 4 is done, and every read of chunk
-// c - 8's comes before the products of chunk c - 6.
+// Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks: chunk c's is written
+// after A and P of chunk c - 2 are formed, so those of chunk c - 3 have been read, which waits
+// for the outputs of chunk c - 6; every read of chunk c - 8's comes before those are.
 struct __align__(16) Info {
     float beta[kC];   // 0 past the chunk's last token
     float ev[kC];     // beta e^{-G}
@@ -147,16 +155,16 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t a, uint
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
                  ::"r"(saddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint32_t tf32(float x) {
-    uint32_t y;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
-    return y;
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&p);
 }
-// D (+)= A B, one 16 x 8 x 8 tile: a = (row g, k t), (g + 8, t), (g, t + 4), (g + 8, t + 4);
-// b = (k t, col g), (t + 4, g); d = (g, 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1), with
-// g = lane / 4, t = lane % 4.
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+// D += A B, one 16 x 8 x 16 fp16 tile: a = (row g, k 2t..), (g + 8, 2t..), (g, 2t + 8..),
+// (g + 8, 2t + 8..); b = (k 2t.., col g), (2t + 8.., g); d = (g, 2t), (g, 2t + 1), (g + 8, 2t),
+// (g + 8, 2t + 1), with g = lane / 4, t = lane % 4.  (The fp16 form: the tf32 one has the same
+// mantissa and took 72 cycles per half as deep a tile.)
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -187,51 +195,56 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *sm
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t0), "r"(smem_u32(smem_src))
                  : "memory");
 }
-__device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+// Four 8 x 8 16-bit tiles; lane 8 m + i gives the address of row i of tile m.
+template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t (&r)[4]) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
 }
 
 // Off-diagonal block of the inverse of a lower-triangular matrix, transposed: Z^T = (T_jj^T
-// A_ij^T) T_ii^T (the caller negates), W x W blocks with leading dimension kLd, T's blocks
-// stored transposed, everything rounded to tf32 where it was stored (T goes on to bf16, eight
-// times coarser).  This warp forms rows j0 .. j0 + 15 (columns of the block) and, of them,
-// columns i0 .. i0 + 15 (rows of the block).
+// A_ij^T) T_ii^T (the caller negates), W x W fp16 blocks with leading dimension kLdT, T's
+// stored transposed.  For unit keys and beta <= 1 every entry of T is at most 1; fp16 keeps 11
+// bits of it, and T goes on to bf16, eight times coarser.  This warp forms rows j0 .. j0 + 15
+// (columns of the block) and, of them, columns i0 .. i0 + 15 (rows of the block).
 template <int W>
-__device__ __forceinline__ void block_product(const float *TjT, const float *A, const float *TiT, int j0, int i0,
-                                              int lane, float (&z)[2][4]) {
-    const int g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void block_product(uint32_t TjT, uint32_t A, uint32_t TiT, int j0, int i0, int lane,
+                                              float (&z)[2][4]) {
     float v[W / 8][4];
 #pragma unroll
     for (int n = 0; n < W / 8; ++n) v[n][0] = v[n][1] = v[n][2] = v[n][3] = 0.f;
-    // 32-bit tiles through the 16-bit matrix load: a row of 16 bytes is four values.
-    const uint32_t pa = smem_u32(TjT + (j0 + (lane & 15)) * kLd + (lane >> 4) * 4);
-    const uint32_t pb = smem_u32(A + (lane & 7) * kLd + (lane >> 3) * 4);
-#pragma unroll 1
-    for (int k = j0; k < W; k += 16) {     // T_jj^T is upper triangular
-        uint32_t a0[4], a1[4];
-        ldmatrix4(pa + 4 * k, a0);
-        ldmatrix4(pa + 4 * k + 32, a1);
+    // Tiles of the A operand: rows 0-7 and 8-15 at k, the same at k + 8; of B (rows n of
+    // A_ij): 0-7 at k and k + 8, 8-15 at k and k + 8.
+    const uint32_t pa = TjT + 2 * ((j0 + (lane & 15)) * kLdT + (lane >> 4) * 8);
+    const uint32_t pb = A + 2 * (((lane & 7) + (lane >> 4) * 8) * kLdT + ((lane >> 3) & 1) * 8);
 #pragma unroll
-        for (int n = 0; n < W / 8; ++n) {
+    for (int k = 0; k < W; k += 16) {
+        if (k < j0) continue;              // T_jj^T is upper triangular
+        uint32_t a[4];
+        ldmatrix4<false>(pa + 2 * k, a);
+#pragma unroll
+        for (int n = 0; n < W / 8; n += 2) {
             uint32_t b[4];
-            ldmatrix4(pb + 4 * (8 * n * kLd + k), b);
-            mma_tf32(v[n], a0, b[0], b[1]);
-            mma_tf32(v[n], a1, b[2], b[3]);
+            ldmatrix4<false>(pb + 2 * (8 * n * kLdT + k), b);
+            mma_f16(v[n], a, b[0], b[1]);
+            mma_f16(v[n + 1], a, b[2], b[3]);
         }
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
-    // The accumulators are the A operand with the contraction index permuted: slot t is
-    // column 2t, slot t + 4 is column 2t + 1; B reads its rows in the same order.
 #pragma unroll
-    for (int k = 0; k < W / 8; ++k) {
-        if (8 * k > i0 + 15) break;        // T_ii is lower triangular
-        const uint32_t a[4] = {tf32(v[k][0]), tf32(v[k][2]), tf32(v[k][1]), tf32(v[k][3])};
-        const float *q = TiT + (8 * k + 2 * t) * kLd + i0 + g;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-            mma_tf32(z[n], a, __float_as_uint(q[8 * n]), __float_as_uint(q[kLd + 8 * n]));
+    for (int k = 0; k < W; k += 16) {
+        if (k > i0) break;                 // T_ii is lower triangular
+        const int n = k / 8;
+        const uint32_t a[4] = {pack_half(v[n][0], v[n][1]), pack_half(v[n][2], v[n][3]),
+                               pack_half(v[n + 1][0], v[n + 1][1]), pack_half(v[n + 1][2], v[n + 1][3])};
+        uint32_t b[4];
+        ldmatrix4<true>(TiT + 2 * ((k + (lane & 15)) * kLdT + i0 + (lane >> 4) * 8), b);
+        mma_f16(z[0], a, b[0], b[1]);
+        mma_f16(z[1], a, b[2], b[3]);
     }
 }
 
@@ -287,16 +300,16 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int s = 0; s < kKQStages; ++s) {
             mbar_init(&bars.kq_full[s], 1);
             mbar_init(&bars.kq_empty[s], 1);
-            mbar_init(&bars.o_full[s], 1);
         }
+        mbar_init(&bars.early_full, 1);
+        for (int s = 0; s < 3; ++s) mbar_init(&bars.drain[s], 1);
+        for (int s = 0; s < kPBufs; ++s) mbar_init(&bars.o_full[s], 1);
         for (int s = 0; s < kInfos; ++s) mbar_init(&bars.info_full[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
             mbar_init(&bars.ap_full[s], 1);
             mbar_init(&bars.w_full[s], 1);
-            mbar_init(&bars.zeroed[s], kGroupThreads);
-            mbar_init(&bars.drain[s], 1);
         }
         mbar_init(&bars.ap_tfree, kGroupThreads);
         mbar_init(&bars.t_ready, kGroupThreads);
@@ -331,11 +344,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         return alive;
     };
     auto wait_info = [&](int c) { return wait(&bars.info_full[c % kInfos], c / kInfos); };
-    // Stage and phase of chunk c in the K/Q ring, advanced chunk by chunk.
+    // Buffer and phase of chunk c among the P buffers, advanced chunk by chunk.
     int stage = 0;
     uint32_t phase = 0;
     auto next_stage = [&] {
-        if (++stage == kKQStages) { stage = 0; phase ^= 1; }
+        if (++stage == kPBufs) { stage = 0; phase ^= 1; }
     };
 
     if (warp < kIntraWarp) {
@@ -419,7 +432,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int group = (warp - kIntraWarp) >> 2, wq = warp & 3, half = wq & 1;
         const int it = 32 * wq + lane, r = it & 63;
         const bool is_p = wq >= 2;
-        float *D0 = (float *)(sm + kOffM + group * kMGroup), *D1 = D0 + kMBlock, *X = D1 + kMBlock;
+        float *diag = (float *)(sm + kOffM + group * kMGroup);
+        uint8_t *tt = sm + kOffM + group * kMGroup + 4 * kMDiag, *X = tt + 2 * kMTT;   // T^T: two blocks
         bool ok = true;
         if (group == 1) { ok = wait_info(0); next_stage(); }
         bool more = group == 0 || (ok && !infos[0].last);
@@ -427,23 +441,6 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int c = group; more; c += 2) {
             ok = ok && wait_info(c);
             const Info &in = infos[c % kInfos];
-            if (in.len < kC) {
-                // Rows past the last token (another sequence's, or unwritten ones) become zeros
-                // in K and V, before any product reads the tiles.
-                ok = ok && wait(&bars.kq_full[stage], phase) && wait(&bars.v_full[c % kVStages], c / kVStages);
-                uint8_t *kt = sm + stage * kKQStage, *vt = sm + kOffV + (c % kVStages) * kVStage;
-#pragma unroll 1
-                for (int e = it; e < (kC - in.len) * 8; e += kGroupThreads) {
-                    const uint32_t at = (uint32_t)(in.len + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    *(uint4 *)(kt + at) = zero;
-                    *(uint4 *)(kt + 16384 + at) = zero;
-                    *(uint4 *)(vt + at) = zero;
-                    *(uint4 *)(vt + 8192 + at) = zero;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.zeroed[group]);
-            }
             // This group's blocks (every thread has read chunk c - 2's) and P's buffer (read by
             // the outputs of chunk c - 3).
             if (c >= 2) ok = ok && wait(&bars.w_full[c & 1], (c >> 1) - 1);
@@ -456,7 +453,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             uint8_t *img = sm + kOffP + stage * 8192;
 #pragma unroll 1
             for (int s0 = 0; s0 < 32 * (1 + half); s0 += 16) {
-                const int lim = (is_p ? r : r - 1) - s0;    // last column kept (15 or more: all)
+                // Last column kept (15 or more: all; none in rows past the last token).
+                const int lim = (r >= in.len ? -1 : is_p ? r : r - 1) - s0;
                 float v[16];
                 tmem_ld16f(tmem_addr(tb, lq, kTAP + s0), v);
                 tmem_ld_wait();
@@ -469,10 +467,19 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             make_uint4(pack(v[i], v[i + 1]), pack(v[i + 2], v[i + 3]), pack(v[i + 4], v[i + 5]),
                                        pack(v[i + 6], v[i + 7]));
                 } else {
-                    float *m = (!half ? D0 : (s0 < 32 ? X : D1)) + (r & 31) * kLd + (s0 & 31);
+                    const int sub = (r >> 4) & 1, rel = s0 - 32 * half;   // this row's 16-block, the tile's
+                    if (rel == 16 * sub) {          // the diagonal block
+                        float *m = diag + (2 * half + sub) * (kMDiag / 4) + (r & 15) * kLdB;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *(uint4 *)&m[i] = make_uint4(tf32(v[i] * br), tf32(v[i + 1] * br), tf32(v[i + 2] * br), tf32(v[i + 3] * br));
+                        for (int i = 0; i < 16; i += 4)
+                            *(float4 *)&m[i] = make_float4(v[i] * br, v[i + 1] * br, v[i + 2] * br, v[i + 3] * br);
+                    } else if (rel < 16 * sub) {    // left of it: fp16 (rel < 0: rows 32-63, columns 0-31)
+                        uint4 *m = (uint4 *)((rel < 0 ? X : tt + half * kMTT) + 2 * ((r & 31) * kLdT + (s0 & 31)));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            m[i] = make_uint4(pack_half(v[8 * i] * br, v[8 * i + 1] * br), pack_half(v[8 * i + 2] * br, v[8 * i + 3] * br),
+                                              pack_half(v[8 * i + 4] * br, v[8 * i + 5] * br), pack_half(v[8 * i + 6] * br, v[8 * i + 7] * br));
+                    }
                 }
             }
             if (is_p) fence_proxy_async_smem();
@@ -483,8 +490,9 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // 16 x 16 block, lane j its column j, four unknowns at a time; then the block
             // between them.
             if (!is_p) {
-                float *Dw = half ? D1 : D0;
-                float *B = Dw + 16 * (lane >> 4) * (kLd + 1);
+                uint8_t *Tw = tt + half * kMTT;
+                const int sub = lane >> 4;
+                const float *B = diag + (2 * half + sub) * (kMDiag / 4);
                 const int j = lane & 15, g = lane >> 2, t = lane & 3;
                 float x[16];
 #pragma unroll
@@ -493,26 +501,28 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int m0 = 0; m0 < 16; m0 += 4) {
 #pragma unroll
                     for (int i = m0 + 1; i < 16; ++i) {
-                        const float4 l = *(const float4 *)&B[i * kLd + m0];
+                        const float4 l = *(const float4 *)&B[i * kLdB + m0];
                         const float lv[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                         for (int m = 0; m < 4; ++m)
                             if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
                     }
                 }
-                __syncwarp();
+                // Transposed: lane j's column is row j of the block.
+                uint4 *p = (uint4 *)(Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub));
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)   // transposed: lane j's column is row j
-                    *(uint4 *)&B[j * kLd + i] = make_uint4(tf32(x[i]), tf32(x[i + 1]), tf32(x[i + 2]), tf32(x[i + 3]));
+                for (int i = 0; i < 2; ++i)
+                    p[i] = make_uint4(pack_half(x[8 * i], x[8 * i + 1]), pack_half(x[8 * i + 2], x[8 * i + 3]),
+                                      pack_half(x[8 * i + 4], x[8 * i + 5]), pack_half(x[8 * i + 6], x[8 * i + 7]));
                 __syncwarp();
                 float z[2][4];
-                block_product<16>(Dw, Dw + 16 * kLd, Dw + 16 * (kLd + 1), 0, 0, lane, z);
+                const uint32_t tw = smem_u32(Tw);
+                block_product<16>(tw, tw + 2 * 16 * kLdT, tw + 2 * (16 * kLdT + 16), 0, 0, lane, z);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t *p = (uint32_t *)&Dw[g * kLd + 16 + 8 * q + 2 * t];
-                    *(uint2 *)p = make_uint2(tf32(-z[q][0]), tf32(-z[q][1]));
-                    *(uint2 *)(p + 8 * kLd) = make_uint2(tf32(-z[q][2]), tf32(-z[q][3]));
-                }
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        *(uint32_t *)(Tw + 2 * ((g + 8 * u) * kLdT + 16 + 8 * q + 2 * t)) = pack_half(-z[q][2 * u], -z[q][2 * u + 1]);
             }
             // T's operands: free once the products of chunk c - 1 have read them.
             if (c > 0) {
@@ -522,11 +532,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (group_sync_any(group, !ok)) break;
             // T's two operands, rows i, columns j: tiles of T^T times the column's factor, stored
             // transposed.
-            const int g = lane >> 2, t = lane & 3;
+            const int g = lane >> 2;
             {   // rows 32-63, columns 0-31: 16 x 16 per warp
                 const int i0 = 16 * half, j0 = 16 * (wq >> 1);
                 float z[2][4];
-                block_product<32>(D0, X, D1, j0, i0, lane, z);
+                block_product<32>(smem_u32(tt), smem_u32(X), smem_u32(tt + kMTT), j0, i0, lane, z);
                 const uint32_t at = sw128_offset(32 + i0 + 8 * (lane >> 4) + (lane & 7), j0 + 8 * ((lane >> 3) & 1), 64);
                 const float be0 = in.beta[j0 + g], be1 = in.beta[j0 + g + 8];
                 const float ev0 = -in.ev[j0 + g], ev1 = -in.ev[j0 + g + 8];
@@ -536,7 +546,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                 pack(z[1][0] * ev0, z[1][1] * ev0), pack(z[1][2] * ev1, z[1][3] * ev1));
             }
             {   // the diagonal blocks: a block and an operand per warp, eight rows at a time
-                const float *Dw = half ? D1 : D0;
+                // Tiles of T^T: columns j of the image in blocks of eight, rows i.
+                const uint32_t tw = smem_u32(tt + half * kMTT) + 2 * lane * kLdT;
                 const uint32_t img = smem_u32(sm + (is_p ? kOffT2 : kOffT1));
                 float fac[4];
 #pragma unroll
@@ -547,13 +558,29 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
                 for (int i = 0; i < 32; i += 8) {
                     uint32_t p[4];
+                    ldmatrix4<false>(tw + 2 * i, p);
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        const float2 x = *(const float2 *)&Dw[(8 * m + g) * kLd + i + 2 * t];
+                        const float2 x = __half22float2(*(const __half2 *)&p[m]);
                         p[m] = 8 * m <= i ? pack(x.x * fac[m], x.y * fac[m]) : 0u;
                     }
                     stmatrix4_trans(img + sw128_offset(32 * half + i + (lane & 7), 32 * half + 8 * (lane >> 3), 64),
                                     p[0], p[1], p[2], p[3]);
+                }
+            }
+            if (in.len < kC) {
+                // Rows past the last token (another sequence's, or unwritten ones) become zeros
+                // in K and V: T's zeros do not undo an infinity or a NaN.
+                ok = ok && wait(&bars.kq_full[c & 1], c >> 1) && wait(&bars.v_full[c & 1], c >> 1);
+                uint8_t *kt = sm + (c & 1) * kKQStage, *vt = sm + kOffV + (c & 1) * kVStage;
+#pragma unroll 1
+                for (int e = it; e < (kC - in.len) * 8; e += kGroupThreads) {
+                    const uint32_t at = (uint32_t)(in.len + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    *(uint4 *)(kt + at) = zero;
+                    *(uint4 *)(kt + 16384 + at) = zero;
+                    *(uint4 *)(vt + at) = zero;
+                    *(uint4 *)(vt + 8192 + at) = zero;
                 }
             }
             fence_proxy_async_smem();
@@ -662,11 +689,11 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
         for (int c = -1; ok; ++c) {
             if (c >= 0) {
-                const int s = stage;
+                const int s = c & 1;
                 const uint32_t st = smem_u32(sm + s * kKQStage);
                 const uint64_t dQ = desc_kmajor_sw128(st + 8192), dK = desc_mnmajor_sw128(st, 16384);
-                const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + s * 8192));
-                ok = wait(&bars.kq_full[s], phase) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
+                const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + stage * 8192));
+                ok = wait(&bars.kq_full[s], c >> 1) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (leader) {   // [F^T] += S^T (-W)^T
@@ -696,7 +723,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_ts(tmem_addr(tb, 0, kTO), fb + 8 * ks, dP + ks * (32 >> 4), id64, true);
-                    mma_commit(&bars.o_full[s]);
+                    mma_commit(&bars.o_full[stage]);
                 }
                 __syncwarp();
                 more = !infos[c % kInfos].last;
@@ -723,43 +750,17 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         __syncwarp();
     } else if (warp == kIssue2Warp) {
-        // --------------------------------------------- issue: A, P and W --
+        // ---------------------------------------------------------- issue: W --
         const bool leader = elect_one();
         const uint64_t dT = desc_kmajor_sw128(smem_u32(sm + kOffT1));
-        int zeros[2] = {0, 0};     // partial chunks of each group so far
-        bool ok = true, more = true;
+        bool ok = true;
 #pragma unroll 1
-        for (int c = -1; ok; ++c) {   // A and P a chunk ahead of W
-            if (more) {               // [AP] = [K; Q] K^T
-                const int d = c + 1, s = stage;
-                ok = wait_info(d) && wait(&bars.kq_full[s], phase);
-                if (ok && infos[d % kInfos].len < kC) {
-                    const int g = d & 1;
-                    ok = wait(&bars.zeroed[g], g ? zeros[1] : zeros[0]);
-                    if (g) ++zeros[1]; else ++zeros[0];
-                }
-                if (d > 0) ok = ok && wait(&bars.ap_tfree, d - 1);
-                if (!ok) break;
-                tc_fence_after_sync();
-                if (leader) {
-                    const uint64_t dKQ = desc_kmajor_sw128(smem_u32(sm + s * kKQStage));
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint64_t x = dKQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
-                        mma_ss(tmem_addr(tb, 0, kTAP), x, x, idesc_bf16_f32(128, 64), ks > 0);
-                    }
-                    mma_commit(&bars.ap_full[d & 1]);
-                }
-                __syncwarp();
-                more = !infos[d % kInfos].last;
-                next_stage();
-            }
-            if (c < 0) continue;
-            ok = wait(&bars.t_ready, c) && (c == 0 || wait(&bars.w_tfree, c - 1));
+        for (int c = 0; ok; ++c) {
+            ok = wait(&bars.kq_full[c & 1], c >> 1) && wait(&bars.t_ready, c) && (c == 0 || wait(&bars.w_tfree, c - 1));
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {   // [W^T] = K^T (-T Diag(beta))^T
-                const uint64_t dK = desc_mnmajor_sw128(smem_u32(sm + (c % kKQStages) * kKQStage), 16384);
+                const uint64_t dK = desc_mnmajor_sw128(smem_u32(sm + (c & 1) * kKQStage), 16384);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_ss(tmem_addr(tb, 0, kTW), dK + ks * (2048 >> 4), dT + ks * (32 >> 4),
@@ -777,7 +778,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == kLoadWarp) {
         // -------------------------------------------------------------- load --
         const bool leader = elect_one();
-        int kq_loaded = 0, v_loaded = 0, start = 0;
+        int start = 0, loaded = 0;
         // Tokens left in the current block, and its index (no blocks: more than there are).
         int to_block = a.block > 0 ? a.block - ctx % a.block : 0x7fffffff, blk = a.block > 0 ? ctx / a.block : 0;
         float g[2], be[2];           // tokens 2 lane, 2 lane + 1 of the next chunk
@@ -804,9 +805,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; ok && start < len; ++c) {
-            const int s = stage, t0 = tbeg + start;
-            // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row,
-            // and the range of e^{-G}; then the factors.
+            // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row, and the
+            // range of e^{-G}; then the factors.
             int m = min(kC, len - start);
             m = min(m, to_block);
             const float x0 = g[0] * kLog2e, x1 = g[1] * kLog2e;
@@ -842,49 +842,81 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 in.len = m;
                 in.last = start + m >= len;
                 in.row = -1;
-                if (m == to_block && blk < a.table_cols) {
+                if (a.block > 0 && m == to_block && blk < a.table_cols) {
                     const int row = a.table[(size_t)n * a.table_cols + blk];
                     if (row >= 0 && row < a.pool_size) in.row = row;
                 }
             }
             __syncwarp();
             if (leader) mbar_arrive(&bars.info_full[c % kInfos]);
-            if (c >= kKQStages && !wait(&bars.kq_empty[s], phase ^ 1)) break;
+            if (c > 0 && !wait(&bars.ap_full[(c - 1) & 1], (c - 1) >> 1)) break;
             if (leader) {
-                uint8_t *st = sm + s * kKQStage;
+                uint8_t *st = sm + kOffEarly;
+                const int t0 = tbeg + start;
+                mbar_arrive_expect_tx(&bars.early_full, kKQStage);
+                tma_tile(st, &tm_k, 0, hk, t0, &bars.early_full);
+                tma_tile(st + 16384, &tm_k, 64, hk, t0, &bars.early_full);
+                tma_tile(st + 8192, &tm_q, 0, hk, t0, &bars.early_full);
+                tma_tile(st + 24576, &tm_q, 64, hk, t0, &bars.early_full);
+            }
+            ++loaded;
+            __syncwarp();
+            prefetch(start + m + kC);
+            // [AP] = [K; Q] K^T, once the previous chunk's A and P have been read.
+            if (!wait(&bars.early_full, c) || (c > 0 && !wait(&bars.ap_tfree, c - 1))) break;
+            tc_fence_after_sync();
+            if (leader) {
+                const uint64_t d = desc_kmajor_sw128(smem_u32(sm + kOffEarly));
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint64_t x = d + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+                    mma_ss(tmem_addr(tb, 0, kTAP), x, x, idesc_bf16_f32(128, 64), ks > 0);
+                }
+                mma_commit(&bars.ap_full[c & 1]);
+            }
+            __syncwarp();
+            start += m;
+            to_block -= m;
+            if (to_block == 0 && a.block > 0) { to_block = a.block; ++blk; }
+            if (start < len) fetch(start);
+        }
+        if (leader) {   // tiles landed and products finished before the CTA may exit
+            if (loaded > 0) mbar_wait(&bars.early_full, (loaded - 1) & 1, globaltimer_ns() + kDrainNs);
+            mma_commit(&bars.drain[2]);
+            mbar_wait(&bars.drain[2], 0, globaltimer_ns() + kDrainNs);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------- load: the other products --
+        const bool leader = elect_one();
+        int loaded = 0;
+#pragma unroll 1
+        for (int c = 0;; ++c) {
+            const int s = c & 1;
+            if (!wait_info(c)) break;
+            if (c >= 2 && !(wait(&bars.kq_empty[s], (c >> 1) - 1) && wait(&bars.v_empty[s], (c >> 1) - 1))) break;
+            const int t0 = tbeg + infos[c % kInfos].start;
+            if (leader) {
+                uint8_t *st = sm + s * kKQStage, *vt = sm + kOffV + s * kVStage;
+                mbar_arrive_expect_tx(&bars.v_full[s], kVStage);
+                tma_tile(vt, &tm_v, 0, h, t0, &bars.v_full[s]);
+                tma_tile(vt + 8192, &tm_v, 64, h, t0, &bars.v_full[s]);
                 mbar_arrive_expect_tx(&bars.kq_full[s], kKQStage);
                 tma_tile(st, &tm_k, 0, hk, t0, &bars.kq_full[s]);
                 tma_tile(st + 16384, &tm_k, 64, hk, t0, &bars.kq_full[s]);
                 tma_tile(st + 8192, &tm_q, 0, hk, t0, &bars.kq_full[s]);
                 tma_tile(st + 24576, &tm_q, 64, hk, t0, &bars.kq_full[s]);
             }
-            ++kq_loaded;
+            ++loaded;
             __syncwarp();
-            if (c >= kVStages && !wait(&bars.v_empty[c & 1], (c >> 1) - 1)) break;
-            if (leader) {
-                uint8_t *vt = sm + kOffV + (c % kVStages) * kVStage;
-                mbar_arrive_expect_tx(&bars.v_full[c & 1], kVStage);
-                tma_tile(vt, &tm_v, 0, h, t0, &bars.v_full[c & 1]);
-                tma_tile(vt + 8192, &tm_v, 64, h, t0, &bars.v_full[c & 1]);
+            if (infos[c % kInfos].last) break;
+        }
+        if (leader)
+#pragma unroll 1
+            for (int c = max(0, loaded - 2); c < loaded; ++c) {
+                mbar_wait(&bars.kq_full[c & 1], (c >> 1) & 1, globaltimer_ns() + kDrainNs);
+                mbar_wait(&bars.v_full[c & 1], (c >> 1) & 1, globaltimer_ns() + kDrainNs);
             }
-            ++v_loaded;
-            __syncwarp();
-            prefetch(start + m + kC);
-            start += m;
-            to_block -= m;
-            if (to_block == 0) { to_block = a.block; ++blk; }
-            if (start < len) fetch(start);
-            next_stage();
-        }
-        // Every tile has landed before the CTA may exit.
-        if (leader) {
-#pragma unroll 1
-            for (int c = max(0, kq_loaded - kKQStages); c < kq_loaded; ++c)
-                mbar_wait(&bars.kq_full[c % kKQStages], (c / kKQStages) & 1, globaltimer_ns() + kDrainNs);
-#pragma unroll 1
-            for (int c = max(0, v_loaded - kVStages); c < v_loaded; ++c)
-                mbar_wait(&bars.v_full[c % kVStages], (c / kVStages) & 1, globaltimer_ns() + kDrainNs);
-        }
         __syncwarp();
     }
     }
