@@ -83,8 +83,8 @@ constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group, see
 constexpr int kLdB = 20, kLdT = 40;
 constexpr uint32_t kMDiag = 16 * kLdB * 4, kMTT = 32 * kLdT * 2;
 constexpr uint32_t kMGroup = 4 * kMDiag + 3 * kMTT;
-constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 2 KiB a warp
-constexpr uint32_t kSmem = kOffO + 4 * 2048 + 1024;
+constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 1 KiB a warp
+constexpr uint32_t kSmem = kOffO + 4 * 1024 + 1024;
 
 // TMEM columns.
 constexpr uint32_t kTS = 0;      // S^T, fp32 [dv][dk]
@@ -133,21 +133,13 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
 }
-// 16 lanes x 64 columns of TMEM as 16 x 8 accumulator tiles: v[4 j ..] holds, of column
+// 16 lanes x 16 columns of TMEM as two 16 x 8 accumulator tiles: r[4 j ..] holds, of column
 // group 8 j, (lane g, columns 2t, 2t + 1) and (lane g + 8, the same columns), with
 // g = thread / 4, t = thread % 4.
-__device__ __forceinline__ void tmem_ld_tiles(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_tiles16(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
 }
 // Four 8 x 8 16-bit tiles, each stored transposed; lane 8 m + i gives the address of row i of
 // tile m.
@@ -189,11 +181,6 @@ __device__ __forceinline__ void tma_tile(void *smem_dst, const CUtensorMap *map,
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int h, int t0) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t0) : "memory");
-}
-__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *smem_src, int x, int h, int t0) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(h), "r"(t0), "r"(smem_u32(smem_src))
-                 : "memory");
 }
 // Four 8 x 8 16-bit tiles; lane 8 m + i gives the address of row i of tile m.
 template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t saddr, uint32_t (&r)[4]) {
@@ -266,8 +253,7 @@ __device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
 
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                 const __grid_constant__ Params prm)
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params prm)
 {
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
@@ -408,7 +394,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 if (last) break;
             }
-#pragma unroll 1
+#pragma unroll
             for (int p = 0; p < 2; ++p) {
                 tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
                 tmem_ld_wait();
@@ -555,7 +541,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const int col = 32 * half + 8 * m + g;
                     fac[m] = is_p ? in.ev[col] : -in.beta[col];
                 }
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < 32; i += 8) {
                     uint32_t p[4];
                     ldmatrix4<false>(tw + 2 * i, p);
@@ -596,7 +582,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp < kIssueWarp) {
         // --------------------------------------------------------------- aux --
         const int wq = warp & 3, it = 32 * wq + lane;
-        uint8_t *ost = sm + kOffO + 2048 * wq;     // two tiles of [16 tokens][32 channels]
+        uint8_t *ost = sm + kOffO + 1024 * wq;     // a tile of [16 tokens][32 channels]
         __nv_bfloat16 *o = (__nv_bfloat16 *)a.o;
         const uint32_t osa = smem_u32(ost) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
         uint32_t xa[32], xb[32];
@@ -605,43 +591,35 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!wait(&bars.o_full[stage], phase)) return false;
             next_stage();
             tc_fence_after_sync();
-            const int m = in.len, t0 = tbeg + in.start;
-            // 16 tokens at a time through two 1 KiB tiles: four 8 x 8 blocks (channels x tokens)
-            // become eight token rows of 32 channels, 16-byte pieces swizzled by token pair.
-            tmem_ld_tiles(tmem_addr(tb, lq, kTO), xa);
-            tmem_ld_tiles(tmem_addr(tb, lq + 16, kTO), xb);
-            tmem_ld_wait();
-            tc_fence_before_sync();
-            mbar_arrive(&bars.o_free);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (16 * q >= m) break;
-                const uint32_t tile = (q & 1) * 1024;
-                if (lane == 0) bulk_wait_read<1>();    // the store before the last has read this tile
-                __syncwarp();
+            // 16 tokens at a time: four 8 x 8 blocks (channels x tokens) become eight token rows of 32
+            // channels, 16-byte pieces swizzled by token pair; a lane then stores two of them.
+#pragma unroll 1
+            for (int q = 0; q < kC; q += 16) {
+                uint32_t u[8], v[8];
+                tmem_ld_tiles16(tmem_addr(tb, lq, kTO + q), u);
+                tmem_ld_tiles16(tmem_addr(tb, lq + 16, kTO + q), v);
+                tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t *u = xa + 8 * q + 4 * j, *v = xb + 8 * q + 4 * j;
-                    const float2 d = *(const float2 *)&in.eo[16 * q + 8 * j + 2 * (lane & 3)];
+                    const float2 d = *(const float2 *)&in.eo[q + 8 * j + 2 * (lane & 3)];
                     auto scaled = [&](const uint32_t *x) {
                         return pack(__uint_as_float(x[0]) * d.x, __uint_as_float(x[1]) * d.y);
                     };
-                    stmatrix4_trans(osa + tile + j * 512, scaled(u), scaled(u + 2), scaled(v), scaled(v + 2));
+                    stmatrix4_trans(osa + j * 512, scaled(u + 4 * j), scaled(u + 4 * j + 2), scaled(v + 4 * j),
+                                    scaled(v + 4 * j + 2));
                 }
-                if (16 * q + 16 > m) break;            // only some of these rows are the chunk's
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) { tma_store(&tm_o, ost + tile, 32 * wq, h, t0 + 16 * q); bulk_commit(); }
-            }
-            if (m & 15) {
-                __syncwarp();
-                const int q = m >> 4;
-#pragma unroll 1
-                for (int e = lane; e < (m & 15) * 4; e += 32)
-                    *(uint4 *)(o + ((size_t)(t0 + 16 * q + (e >> 2)) * a.H + h) * kD + 32 * wq + 8 * (e & 3)) =
-                        *(const uint4 *)(ost + (q & 1) * 1024 + (e >> 2) * 64 + (((e & 3) ^ ((e >> 3) & 3)) << 4));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int t = q + 8 * j + (lane >> 2);
+                    const uint4 w = *(const uint4 *)(ost + j * 512 + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
+                    if (t < in.len)
+                        *(uint4 *)(o + ((size_t)(tbeg + in.start + t) * a.H + h) * kD + 32 * wq + 8 * (lane & 3)) = w;
+                }
                 __syncwarp();
             }
+            tc_fence_before_sync();
+            mbar_arrive(&bars.o_free);
             return true;
         };
         bool ok = true;
@@ -675,8 +653,6 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (c > 0) ok = output(c - 1);
             if (!chunk) break;
         }
-        if (lane == 0) bulk_wait<0>();   // every store has completed before the CTA exits
-        __syncwarp();
     } else {
     if (warp == kIssueWarp) {
         // ------------------------------------------------------------- issue --
@@ -781,8 +757,9 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int start = 0, loaded = 0;
         // Tokens left in the current block, and its index (no blocks: more than there are).
         int to_block = a.block > 0 ? a.block - ctx % a.block : 0x7fffffff, blk = a.block > 0 ? ctx / a.block : 0;
-        float g[2], be[2];           // tokens 2 lane, 2 lane + 1 of the next chunk
-        auto fetch = [&](int from) {
+        // g and beta of tokens 2 lane, 2 lane + 1 of this chunk, and of the next if this one is full.
+        float g[2], be[2], gn[2], bn[2];
+        auto fetch = [&](int from, float (&g)[2], float (&be)[2]) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = from + 2 * lane + u;
@@ -800,13 +777,14 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tma_prefetch(&tm_v, x, h, tbeg + t);
             }
         };
-        fetch(0);
+        fetch(0, g, be);
         prefetch(kC);
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; ok && start < len; ++c) {
             // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row, and the
             // range of e^{-G}; then the factors.
+            fetch(start + kC, gn, bn);
             int m = min(kC, len - start);
             m = min(m, to_block);
             const float x0 = g[0] * kLog2e, x1 = g[1] * kLog2e;
@@ -878,7 +856,12 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             start += m;
             to_block -= m;
             if (to_block == 0 && a.block > 0) { to_block = a.block; ++blk; }
-            if (start < len) fetch(start);
+            if (m == kC) {
+                g[0] = gn[0]; g[1] = gn[1];
+                be[0] = bn[0]; be[1] = bn[1];
+            } else if (start < len) {
+                fetch(start, g, be);
+            }
         }
         if (leader) {   // tiles landed and products finished before the CTA may exit
             if (loaded > 0) mbar_wait(&bars.early_full, (loaded - 1) & 1, globaltimer_ns() + kDrainNs);
@@ -935,12 +918,12 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream)
     if (ctas == 0) return cudaSuccess;
     cudaError_t err = cudaFuncSetAttribute(gdr_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (err != cudaSuccess) return err;
-    CUtensorMap mq, mk, mv, mo;
+    CUtensorMap mq, mk, mv;
     memset(&mq, 0, sizeof(mq));
-    mk = mv = mo = mq;   // with no tokens no tile is read or written
+    mk = mv = mq;   // with no tokens no tile is read
     if (a.total_tokens > 0 &&
         (!tc_rows_map(&mq, a.q, a.total_tokens, a.Hk) || !tc_rows_map(&mk, a.k, a.total_tokens, a.Hk) ||
-         !tc_rows_map(&mv, a.v, a.total_tokens, a.H) || !tc_out_map32(&mo, a.o, a.total_tokens, a.H)))
+         !tc_rows_map(&mv, a.v, a.total_tokens, a.H)))
         return cudaErrorInvalidValue;
     // Longest sequences first (they set the end of the launch); the host offsets only
     // order the CTAs, each of which reads its own bounds on the device.
@@ -961,7 +944,7 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream)
             p.order[at] = (uint16_t)i;
         }
     }
-    gdr_chunk_kernel<<<(unsigned)ctas, kThreads, kSmem, stream>>>(mq, mk, mv, mo, p);
+    gdr_chunk_kernel<<<(unsigned)ctas, kThreads, kSmem, stream>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 

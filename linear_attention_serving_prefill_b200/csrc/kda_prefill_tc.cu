@@ -1712,17 +1712,16 @@ bool encode_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H)
 // o [T][H][128] bf16 as a 3-D tensor (channel, head, token) with a {128, 1, 64}
 // box and no swizzle: one chunk's output rows of one head per TMA store, from
 // a dense [64][128] staging tile.
-bool encode_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t channels = kDV,
-                    uint32_t tokens = kChunk, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE)
+bool encode_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H)
 {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kDV, (cuuint64_t)H, (cuuint64_t)(T > 0 ? T : 1)};
     const cuuint64_t strides[2] = {(cuuint64_t)kDV * 2, (cuuint64_t)H * kDV * 2};
-    const cuuint32_t box[3] = {(cuuint32_t)channels, 1, (cuuint32_t)tokens};
+    const cuuint32_t box[3] = {(cuuint32_t)kDV, 1, (cuuint32_t)kChunk};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1731,11 +1730,6 @@ bool encode_out_map(CUtensorMap *map, void *base, int32_t T, int32_t H, uint32_t
 bool tc_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H)
 {
     return encode_rows_map(map, base, T, H);
-}
-
-bool tc_out_map32(CUtensorMap *map, void *base, int32_t T, int32_t H)
-{
-    return encode_out_map(map, base, T, H, 32, 16, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 namespace {

@@ -31,10 +31,6 @@ size_t tc_workspace_bytes(int32_t total_tokens, int32_t num_seqs, int32_t H, int
 // and the 128-byte swizzle; false when the driver refuses it.
 bool tc_rows_map(CUtensorMap *map, const void *base, int32_t T, int32_t H);
 
-// Tensor map of [T][H][128] bf16 output rows with a {32 channels, 1 head, 16 tokens}
-// box and the 64-byte swizzle.
-bool tc_out_map32(CUtensorMap *map, void *base, int32_t T, int32_t H);
-
 // Launches plan, intra-chunk and state kernels on `stream`, then, when
 // a.segments > 1, the segment composition and the output correction.
 cudaError_t launch_prefill_tensor_core(const PrefillArgs &a, cudaStream_t stream);
