@@ -8,35 +8,41 @@
 //   o_r = scale (e^{G_r} S^T q_r + sum_{s<=r} (q_r . k_s) e^{G_r - G_s} E_s),
 //   S <- e^{G_C} S + sum_s e^{G_C - G_s} k_s E_s^T.
 // In the variables F_r = e^{-G_r} E_r every decay leaves the sums:
-//   T = (I + strictly_lower(Diag(beta) K K^T))^{-1},  P = lower(Q K^T),  W = T Diag(beta) K,
-//   F = T Diag(beta e^{-G}) V - W S,  o_r = scale e^{G_r} (Q S + P F)_r,
-//   S <- e^{G_C} (S + K^T F),
-// so one factor per token remains at T's columns, one at the outputs and one at the
-// state; K, Q and V enter the products as their TMA tiles.  e^{-G} has to stay in the
-// floating-point range: a chunk ends early, before the token at which |G| would pass
-// 2^kRange; below 2^kSafe nothing is shifted, between them the chunk's scale is shifted
-// down so that e^{-G} <= 2^kSafe (state entries below 2^-26 are then lost in that
-// chunk, which multiplies the state by less than 2^-100 anyway).  Relative accuracy
-// is that of the decayed form: each term is scaled by a power it keeps to its use.
+//   T = (I + strictly_lower(Diag(beta) K K^T))^{-1},  P = lower(Q K^T),
+//   R_r = beta_r (e^{-G_r} v_r - S^T k_r),  F = T R,
+//   o_r = scale e^{G_r} (Q S + P F)_r,  S <- e^{G_C} (S + K^T F),
+// so one factor per token remains in R, one at the outputs and one at the state, and K and Q
+// enter the products as their TMA tiles.  e^{-G} has to stay in the floating-point range: a
+// chunk ends early, before the token at which |G| would pass 2^kRange; below 2^kSafe nothing
+// is shifted, between them the chunk's scale is shifted down so that e^{-G} <= 2^kSafe (state
+// entries below 2^-26 are then lost in that chunk, which multiplies the state by less than
+// 2^-100 anyway).  Relative accuracy is that of the decayed form: each term is scaled by a
+// power it keeps to its use.
 //
-// One CTA of 24 warps owns a (sequence, value head) and walks its chunks with the fp32
-// state transposed in tensor memory.  Nothing goes through HBM but q, k, v, g, beta,
-// o and the state rows.  Roles:
-//   chain (warps 0-7)    F^T from its accumulator to a bf16 operand; S^T times its
-//                        factor, to the fp32 master and its bf16 copy;
+// Precision.  K and Q are exact operands.  The others on the state's path, S, R, T and F, are
+// each the sum of two bf16 numbers (17 bits), and a product of two such sums leaves out only
+// low x low: the state comes out within about 1e-5 of the recurrence in 64 bits (2-norm),
+// where single bf16 operands gave 2.5e-3.  The outputs' own products take the high parts
+// alone, which their rounding to bf16 hides.
+//
+// One CTA of 23 warps owns a (sequence, value head) and walks its chunks with the fp32 state
+// transposed in tensor memory.  Nothing goes through HBM but q, k, v, g, beta, o and the
+// state rows.  Roles:
+//   chain (warps 0-7)    S^T K^T to R^T, F^T, and S^T times its factor, each from its
+//                        accumulator to two bf16 operands; the fp32 master;
 //   intra (warps 8-15)   two groups, even and odd chunks: A and P from the accumulator,
 //                        T by 16 x 16 forward substitution (fp32) and two block doublings
-//                        (fp16 warp products), T's two bf16 operands;
-//   aux   (warps 16-19)  W^T from its accumulator to a bf16 operand, O^T to o;
-//   issue (warps 20, 21) the products of the state chain; W's;
-//   load  (warps 22, 23) chunk bounds and factors (a warp scan), the K and Q tiles for A and P
-//                        and their product; K, Q and V for the other products.
+//                        (warp products of split fp16), T's two bf16 operands;
+//   aux   (warps 16-19)  O^T to o;
+//   issue (warp 20)      the products of the state chain;
+//   load  (warps 21, 22) chunk bounds and factors (a warp scan), the K and Q tiles for A and P
+//                        and their product; K, Q and V for the chain.
 // K and Q are loaded twice (the second time from L2): A and P are formed up to three chunks
 // ahead of the state, and a tile that stayed for both uses would sit idle in between.
 // Products (TMEM accumulators in brackets), chunk c:
-//   [AP] = [K; Q] K^T;  [W^T] = K^T (-T Diag(beta))^T;  [F^T] = V^T (T Diag(beta e^{-G}))^T
-//   [F^T] += S^T (-W)^T;  [O^T] = S^T Q^T;  [S^T] += F^T K;  [O^T] += F^T P^T
-// K^T, V^T and W^T are MN-major operands, so no tile is ever transposed.
+//   [AP] = [K; Q] K^T;  [DF] = S^T K^T;  [O^T] = S^T Q^T;  [DF] = R^T T^T;
+//   [S^T] += F^T K;  [O^T] += F^T P^T
+// K is an MN-major operand of the state's product, so no tile is ever transposed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -58,11 +64,11 @@ constexpr int kD = 128, kC = 64;              // head size, chunk
 // take microseconds.
 constexpr uint32_t kTries = 1u << 20, kSuspendNs = 2000;
 constexpr uint64_t kDrainNs = 2000000000ull;   // limit of the waits at the end of a role
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRange = 200.f, kSafe = 100.f;   // log2 bounds of e^{-G}, see above
+constexpr double kLog2e = 1.4426950408889634;
+constexpr double kRange = 200., kSafe = 100.;   // log2 bounds of e^{-G}, see above
 
 constexpr int kChainThreads = 256, kGroupThreads = 128, kAuxThreads = 128;
-constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kIssue2Warp = 21, kLoadWarp = 22, kLoad2Warp = 23;
+constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kLoadWarp = 21, kLoad2Warp = 22;
 constexpr int kThreads = (kLoad2Warp + 1) * 32;
 
 // Shared memory (offsets from a 1024-aligned base).  A K/Q stage is
@@ -72,36 +78,34 @@ constexpr uint32_t kKQStage = 32768, kVStage = 16384;
 constexpr int kKQStages = 2, kVStages = 2, kInfos = 8, kPBufs = 3;
 constexpr uint32_t kOffEarly = kKQStages * kKQStage;     // the K/Q tile for A and P
 constexpr uint32_t kOffV = kOffEarly + kKQStage;
-constexpr uint32_t kOffW = kOffV + kVStages * kVStage;   // W^T: 128 channels x 64 tokens
-constexpr uint32_t kOffP = kOffW + 16384;                // P: 64 x 64, three buffers
-constexpr uint32_t kOffT1 = kOffP + kPBufs * 8192;            // -T Diag(beta): 64 x 64
-constexpr uint32_t kOffT2 = kOffT1 + 8192;               // T Diag(beta e^{-G})
-constexpr uint32_t kOffM = kOffT2 + 8192;                // per intra group, see below
-// A's four 16 x 16 diagonal blocks in fp32 (rows padded to 20); the two 32 x 32 diagonal blocks
-// of T, transposed, in fp16 (rows padded to 40; A's own block between two diagonal ones sits in
-// the unused lower left); A's rows 32-63, columns 0-31 in fp16.
+constexpr uint32_t kOffP = kOffV + kVStages * kVStage;   // P: 64 x 64, three buffers
+constexpr uint32_t kOffT = kOffP + kPBufs * 8192;        // T: 64 x 64, high and low parts
+constexpr uint32_t kOffM = kOffT + 2 * 8192;             // per intra group, see below
+// A's four 16 x 16 diagonal blocks in fp32 (rows padded to 20), then fp16 blocks of 32 rows
+// (padded to 40), high and low parts: the two 32 x 32 diagonal blocks of T, transposed (A's own
+// block between two diagonal ones sits in the unused lower left); A's rows 32-63, columns 0-31.
 constexpr int kLdB = 20, kLdT = 40;
 constexpr uint32_t kMDiag = 16 * kLdB * 4, kMTT = 32 * kLdT * 2;
-constexpr uint32_t kMGroup = 4 * kMDiag + 3 * kMTT;
+constexpr uint32_t kMLow = 3 * kMTT;                     // from a high part to its low part
+constexpr uint32_t kMGroup = 4 * kMDiag + 2 * kMLow;
 constexpr uint32_t kOffO = (kOffM + 2 * kMGroup + 1023) / 1024 * 1024;   // output staging, 1 KiB a warp
 constexpr uint32_t kSmem = kOffO + 4 * 1024 + 1024;
 
 // TMEM columns.
 constexpr uint32_t kTS = 0;      // S^T, fp32 [dv][dk]
-constexpr uint32_t kTSb = 128;   // its bf16 copy
-constexpr uint32_t kTF = 192;    // F^T accumulator [dv][token]
-constexpr uint32_t kTFb = 256;   // F^T bf16
-constexpr uint32_t kTO = 320;    // O^T accumulator
-constexpr uint32_t kTAP = 384;   // A and P accumulators (rows 0-63, 64-127)
-constexpr uint32_t kTW = 448;    // W^T accumulator [dk][token]
+constexpr uint32_t kTSb = 128;   // its bf16 parts: high, low (64 columns each)
+constexpr uint32_t kTDF = 256;   // accumulator [dv][token]: S^T K^T, then F^T
+constexpr uint32_t kTRF = 320;   // R^T, then F^T, bf16: high, low (32 columns each)
+constexpr uint32_t kTO = 384;    // O^T accumulator
+constexpr uint32_t kTAP = 448;   // A and P accumulators (rows 0-63, 64-127)
 
 struct Bars {
     uint64_t early_full, kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos];
-    uint64_t v_full[kVStages], v_empty[kVStages];   // v_empty: the product with V and T is done
-    uint64_t ap_full[2], o_full[kPBufs], w_full[2];
-    uint64_t ap_tfree, t_ready, w_tfree, w_ready;
-    uint64_t s_ready, f_ready, f_full, s_full, o_free;
-    uint64_t drain[3];
+    uint64_t v_full[kVStages], v_empty[kVStages];
+    uint64_t ap_full[2], o_full[kPBufs], t_free[2];
+    uint64_t ap_tfree, t_ready;
+    uint64_t s_ready, d_full, r_ready, f_full, f_ready, s_full, o_free;
+    uint64_t drain[2];
 };
 
 // Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks: chunk c's is written
@@ -129,6 +133,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^x for |x| up to kSafe and 1, its argument's whole part taken off in 64 bits.
+__device__ __forceinline__ float pow2(double x) {
+    const double n = rint(x);
+    return ex2((float)(x - n)) * __int_as_float(((int)n + 127) << 23);
+}
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
@@ -150,6 +159,17 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t a, uint
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
+}
+// x = hi + lo in bf16 (fp16) pairs: hi the rounded value, lo the rounded rest.
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack(a, b);
+    const float2 r = __fadd2_rn(make_float2(a, b), make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u)));
+    lo = pack(r.x, r.y);
+}
+__device__ __forceinline__ void split_half(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack_half(a, b);
+    const float2 h = __half22float2(*(const __half2 *)&hi);
+    lo = pack_half(a - h.x, b - h.y);
 }
 // D += A B, one 16 x 8 x 16 fp16 tile: a = (row g, k 2t..), (g + 8, 2t..), (g, 2t + 8..),
 // (g + 8, 2t + 8..); b = (k 2t.., col g), (2t + 8.., g); d = (g, 2t), (g, 2t + 1), (g + 8, 2t),
@@ -193,10 +213,11 @@ template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t saddr, 
 }
 
 // Off-diagonal block of the inverse of a lower-triangular matrix, transposed: Z^T = (T_jj^T
-// A_ij^T) T_ii^T (the caller negates), W x W fp16 blocks with leading dimension kLdT, T's
-// stored transposed.  For unit keys and beta <= 1 every entry of T is at most 1; fp16 keeps 11
-// bits of it, and T goes on to bf16, eight times coarser.  This warp forms rows j0 .. j0 + 15
-// (columns of the block) and, of them, columns i0 .. i0 + 15 (rows of the block).
+// A_ij^T) T_ii^T (the caller negates), W x W blocks with leading dimension kLdT, T's stored
+// transposed, every matrix in two fp16 parts (22 bits) kMLow bytes apart, of whose products
+// all but low x low are taken.  For unit keys and beta <= 1 every entry of T is at most 1.
+// This warp forms rows j0 .. j0 + 15 (columns of the block) and, of them, columns
+// i0 .. i0 + 15 (rows of the block).
 template <int W>
 __device__ __forceinline__ void block_product(uint32_t TjT, uint32_t A, uint32_t TiT, int j0, int i0, int lane,
                                               float (&z)[2][4]) {
@@ -207,17 +228,22 @@ __device__ __forceinline__ void block_product(uint32_t TjT, uint32_t A, uint32_t
     // A_ij): 0-7 at k and k + 8, 8-15 at k and k + 8.
     const uint32_t pa = TjT + 2 * ((j0 + (lane & 15)) * kLdT + (lane >> 4) * 8);
     const uint32_t pb = A + 2 * (((lane & 7) + (lane >> 4) * 8) * kLdT + ((lane >> 3) & 1) * 8);
-#pragma unroll
-    for (int k = 0; k < W; k += 16) {
-        if (k < j0) continue;              // T_jj^T is upper triangular
-        uint32_t a[4];
-        ldmatrix4<false>(pa + 2 * k, a);
+#pragma unroll 1
+    for (int k = j0; k < W; k += 16) {     // T_jj^T is upper triangular
+        uint32_t ah[4], al[4];
+        ldmatrix4<false>(pa + 2 * k, ah);
+        ldmatrix4<false>(pa + 2 * k + kMLow, al);
 #pragma unroll
         for (int n = 0; n < W / 8; n += 2) {
-            uint32_t b[4];
-            ldmatrix4<false>(pb + 2 * (8 * n * kLdT + k), b);
-            mma_f16(v[n], a, b[0], b[1]);
-            mma_f16(v[n + 1], a, b[2], b[3]);
+            uint32_t bh[4], bl[4];
+            ldmatrix4<false>(pb + 2 * (8 * n * kLdT + k), bh);
+            ldmatrix4<false>(pb + 2 * (8 * n * kLdT + k) + kMLow, bl);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                mma_f16(v[n + u], ah, bl[2 * u], bl[2 * u + 1]);
+                mma_f16(v[n + u], al, bh[2 * u], bh[2 * u + 1]);
+                mma_f16(v[n + u], ah, bh[2 * u], bh[2 * u + 1]);
+            }
         }
     }
 #pragma unroll
@@ -226,12 +252,20 @@ __device__ __forceinline__ void block_product(uint32_t TjT, uint32_t A, uint32_t
     for (int k = 0; k < W; k += 16) {
         if (k > i0) break;                 // T_ii is lower triangular
         const int n = k / 8;
-        const uint32_t a[4] = {pack_half(v[n][0], v[n][1]), pack_half(v[n][2], v[n][3]),
-                               pack_half(v[n + 1][0], v[n + 1][1]), pack_half(v[n + 1][2], v[n + 1][3])};
-        uint32_t b[4];
-        ldmatrix4<true>(TiT + 2 * ((k + (lane & 15)) * kLdT + i0 + (lane >> 4) * 8), b);
-        mma_f16(z[0], a, b[0], b[1]);
-        mma_f16(z[1], a, b[2], b[3]);
+        uint32_t ah[4], al[4], bh[4], bl[4];
+        split_half(v[n][0], v[n][1], ah[0], al[0]);
+        split_half(v[n][2], v[n][3], ah[1], al[1]);
+        split_half(v[n + 1][0], v[n + 1][1], ah[2], al[2]);
+        split_half(v[n + 1][2], v[n + 1][3], ah[3], al[3]);
+        const uint32_t p = TiT + 2 * ((k + (lane & 15)) * kLdT + i0 + (lane >> 4) * 8);
+        ldmatrix4<true>(p, bh);
+        ldmatrix4<true>(p + kMLow, bl);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            mma_f16(z[u], ah, bl[2 * u], bl[2 * u + 1]);
+            mma_f16(z[u], al, bh[2 * u], bh[2 * u + 1]);
+            mma_f16(z[u], ah, bh[2 * u], bh[2 * u + 1]);
+        }
     }
 }
 
@@ -288,29 +322,29 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(&bars.kq_empty[s], 1);
         }
         mbar_init(&bars.early_full, 1);
-        for (int s = 0; s < 3; ++s) mbar_init(&bars.drain[s], 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&bars.drain[s], 1);
         for (int s = 0; s < kPBufs; ++s) mbar_init(&bars.o_full[s], 1);
         for (int s = 0; s < kInfos; ++s) mbar_init(&bars.info_full[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.v_full[s], 1);
-            mbar_init(&bars.v_empty[s], 1);
+            mbar_init(&bars.v_empty[s], kChainThreads);
             mbar_init(&bars.ap_full[s], 1);
-            mbar_init(&bars.w_full[s], 1);
+            mbar_init(&bars.t_free[s], 1);
         }
         mbar_init(&bars.ap_tfree, kGroupThreads);
         mbar_init(&bars.t_ready, kGroupThreads);
-        mbar_init(&bars.w_tfree, kAuxThreads);
-        mbar_init(&bars.w_ready, kAuxThreads);
         mbar_init(&bars.s_ready, kChainThreads);
-        mbar_init(&bars.f_ready, kChainThreads);
+        mbar_init(&bars.d_full, 1);
+        mbar_init(&bars.r_ready, kChainThreads);
         mbar_init(&bars.f_full, 1);
+        mbar_init(&bars.f_ready, kChainThreads);
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.o_free, kAuxThreads);
         fence_mbar_init();
     }
-    // The upper right quadrants of P and T's operands are zero in every chunk.
+    // The upper right quadrants of P and T are zero in every chunk.
     for (int e = tid; e < (kPBufs + 2) * 128; e += kThreads) {
-        const uint32_t img = kOffP + (e >> 7) * 8192;   // P's buffers, then T's operands
+        const uint32_t img = kOffP + (e >> 7) * 8192;   // P's buffers, then T's parts
         *(uint4 *)(sm + img + sw128_offset((e >> 2) & 31, 32 + 8 * (e & 3), 64)) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
@@ -341,40 +375,89 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // ------------------------------------------------------------- chain --
         const int j = tid & 127, hh = warp >> 2;   // value channel; half of tokens / key channels
         const float *S0 = src >= 0 ? row_of(src) + (size_t)(64 * hh) * kD + j : nullptr;
+        // 32 columns of an accumulator as two bf16 operands of 16 columns each.
+        auto put = [&](const uint32_t (&x)[32], uint32_t hi, uint32_t lo) {
+            uint32_t h[16], l[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) split(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), h[i], l[i]);
+            tmem_st16(tmem_addr(tb, lq, hi), h);
+            tmem_st16(tmem_addr(tb, lq, lo), l);
+        };
+        auto hand_over = [&](uint64_t *bar) {
+            tmem_st_wait();
+            tc_fence_before_sync();
+            mbar_arrive(bar);
+        };
         bool ok = wait_info(0);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
-            uint32_t x[32], y[16];
+            uint32_t x[32];
             const float f = infos[0].in;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 x[i] = S0 ? __float_as_uint(S0[(size_t)(32 * p + i) * kD] * f) : 0u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh + 16 * p), y);
             tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
+            put(x, kTSb + 32 * hh + 16 * p, kTSb + 64 + 32 * hh + 16 * p);
         }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        mbar_arrive(&bars.s_ready);
+        hand_over(&bars.s_ready);
 #pragma unroll 1
         for (int c = 0; ok; ++c) {
-            uint32_t x[32], y[16];
+            uint32_t x[32];
             const Info &in = infos[c % kInfos];
             const bool last = in.last != 0;
             const float out = in.out;
-            // F^T of this half's 32 tokens -> bf16.
+            // V of this thread's channel and half of the tokens, packed by pairs.
+            ok = wait(&bars.v_full[c & 1], c >> 1);
+            uint32_t v[16];
+            {
+                const uint8_t *vt = sm + kOffV + (c & 1) * kVStage + (j >> 6) * 8192 + 32 * hh * 128;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const uint32_t a0 = *(const uint16_t *)(vt + sw128_offset(i, j & 63, 64));
+                    const uint32_t a1 = *(const uint16_t *)(vt + sw128_offset(i + 1, j & 63, 64));
+                    v[i / 2] = a0 | (a1 << 16);
+                }
+            }
+            mbar_arrive(&bars.v_empty[c & 1]);
+            if (in.len < kC) {
+                // K's rows past the last token (another sequence's, or unwritten ones) become
+                // zeros: F's zeros there do not undo an infinity or a NaN.
+                ok = ok && wait(&bars.kq_full[c & 1], c >> 1);
+                uint8_t *kt = sm + (c & 1) * kKQStage;
+#pragma unroll 1
+                for (int e = tid; e < (kC - in.len) * 16; e += kChainThreads)
+                    *(uint4 *)(kt + (e & 8) * 2048 + (in.len + (e >> 4)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            // R^T = beta (e^{-G} V^T - S^T K^T).
+            ok = ok && wait(&bars.d_full, c);
+            if (!ok) break;
+            tc_fence_after_sync();
+            tmem_ld32(tmem_addr(tb, lq, kTDF + 32 * hh), x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 be = *(const float4 *)&in.beta[32 * hh + i], ev = *(const float4 *)&in.ev[32 * hh + i];
+                const uint32_t v0 = v[i / 2], v1 = v[i / 2 + 1];
+                x[i] = __float_as_uint(fmaf(-be.x, __uint_as_float(x[i]), ev.x * __uint_as_float(v0 << 16)));
+                x[i + 1] = __float_as_uint(fmaf(-be.y, __uint_as_float(x[i + 1]), ev.y * __uint_as_float(v0 & 0xFFFF0000u)));
+                x[i + 2] = __float_as_uint(fmaf(-be.z, __uint_as_float(x[i + 2]), ev.z * __uint_as_float(v1 << 16)));
+                x[i + 3] = __float_as_uint(fmaf(-be.w, __uint_as_float(x[i + 3]), ev.w * __uint_as_float(v1 & 0xFFFF0000u)));
+            }
+            if (in.len < kC) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 32 * hh + i < in.len ? x[i] : 0u;
+            }
+            put(x, kTRF + 16 * hh, kTRF + 32 + 16 * hh);
+            hand_over(&bars.r_ready);
+            // F^T = R^T T^T.
             ok = wait(&bars.f_full, c);
             if (!ok) break;
             tc_fence_after_sync();
-            tmem_ld32(tmem_addr(tb, lq, kTF + 32 * hh), x);
+            tmem_ld32(tmem_addr(tb, lq, kTDF + 32 * hh), x);
             tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            tmem_st16(tmem_addr(tb, lq, kTFb + 16 * hh), y);
-            tmem_st_wait();
-            tc_fence_before_sync();
-            mbar_arrive(&bars.f_ready);
+            put(x, kTRF + 16 * hh, kTRF + 32 + 16 * hh);
+            hand_over(&bars.f_ready);
             const int row = in.row;
             if (!last) ok = wait_info(c + 1);
             const float f = last ? 0.f : out * infos[(c + 1) % kInfos].in;
@@ -394,24 +477,21 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 if (last) break;
             }
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < 2; ++p) {
                 tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 t = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 t = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
                                                 make_float2(f, f));
-                    x[2 * i] = __float_as_uint(t.x);
-                    x[2 * i + 1] = __float_as_uint(t.y);
-                    y[i] = pack(t.x, t.y);
+                    x[i] = __float_as_uint(t.x);
+                    x[i + 1] = __float_as_uint(t.y);
                 }
-                tmem_st16(tmem_addr(tb, lq, kTSb + 32 * hh + 16 * p), y);
                 tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
+                put(x, kTSb + 32 * hh + 16 * p, kTSb + 64 + 32 * hh + 16 * p);
             }
-            tmem_st_wait();
-            tc_fence_before_sync();
-            mbar_arrive(&bars.s_ready);
+            hand_over(&bars.s_ready);
         }
     } else if (warp < kAuxWarp) {
         // ------------------------------------------------------------- intra --
@@ -419,7 +499,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int it = 32 * wq + lane, r = it & 63;
         const bool is_p = wq >= 2;
         float *diag = (float *)(sm + kOffM + group * kMGroup);
-        uint8_t *tt = sm + kOffM + group * kMGroup + 4 * kMDiag, *X = tt + 2 * kMTT;   // T^T: two blocks
+        uint8_t *tt = sm + kOffM + group * kMGroup + 4 * kMDiag, *X = tt + 2 * kMTT;   // T^T: two blocks; A
         bool ok = true;
         if (group == 1) { ok = wait_info(0); next_stage(); }
         bool more = group == 0 || (ok && !infos[0].last);
@@ -429,7 +509,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const Info &in = infos[c % kInfos];
             // This group's blocks (every thread has read chunk c - 2's) and P's buffer (read by
             // the outputs of chunk c - 3).
-            if (c >= 2) ok = ok && wait(&bars.w_full[c & 1], (c >> 1) - 1);
+            if (c >= 2) ok = ok && wait(&bars.t_free[c & 1], (c >> 1) - 1);
             if (c >= kPBufs) ok = ok && wait(&bars.o_full[stage], phase ^ 1);
             const float br = in.beta[r];
             ok = ok && wait(&bars.ap_full[c & 1], c >> 1);
@@ -461,10 +541,14 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             *(float4 *)&m[i] = make_float4(v[i] * br, v[i + 1] * br, v[i + 2] * br, v[i + 3] * br);
                     } else if (rel < 16 * sub) {    // left of it: fp16 (rel < 0: rows 32-63, columns 0-31)
                         uint4 *m = (uint4 *)((rel < 0 ? X : tt + half * kMTT) + 2 * ((r & 31) * kLdT + (s0 & 31)));
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            m[i] = make_uint4(pack_half(v[8 * i] * br, v[8 * i + 1] * br), pack_half(v[8 * i + 2] * br, v[8 * i + 3] * br),
-                                              pack_half(v[8 * i + 4] * br, v[8 * i + 5] * br), pack_half(v[8 * i + 6] * br, v[8 * i + 7] * br));
+                        for (int i = 0; i < 8; ++i) split_half(v[2 * i] * br, v[2 * i + 1] * br, hi[i], lo[i]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            m[i] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+                            m[kMLow / 16 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                        }
                     }
                 }
             }
@@ -497,9 +581,13 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // Transposed: lane j's column is row j of the block.
                 uint4 *p = (uint4 *)(Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub));
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    p[i] = make_uint4(pack_half(x[8 * i], x[8 * i + 1]), pack_half(x[8 * i + 2], x[8 * i + 3]),
-                                      pack_half(x[8 * i + 4], x[8 * i + 5]), pack_half(x[8 * i + 6], x[8 * i + 7]));
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) split_half(x[8 * i + 2 * u], x[8 * i + 2 * u + 1], hi[u], lo[u]);
+                    p[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    p[kMLow / 16 + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
                 __syncwarp();
                 float z[2][4];
                 const uint32_t tw = smem_u32(Tw);
@@ -507,67 +595,45 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        *(uint32_t *)(Tw + 2 * ((g + 8 * u) * kLdT + 16 + 8 * q + 2 * t)) = pack_half(-z[q][2 * u], -z[q][2 * u + 1]);
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t *to = (uint32_t *)(Tw + 2 * ((g + 8 * u) * kLdT + 16 + 8 * q + 2 * t));
+                        split_half(-z[q][2 * u], -z[q][2 * u + 1], to[0], to[kMLow / 4]);
+                    }
             }
-            // T's operands: free once the products of chunk c - 1 have read them.
-            if (c > 0) {
-                ok = ok && wait(&bars.w_full[(c - 1) & 1], (c - 1) >> 1);
-                ok = ok && wait(&bars.v_empty[(c - 1) & 1], (c - 1) >> 1);
-            }
+            // T's operands: free once chunk c - 1's product has read them.
+            if (c > 0) ok = ok && wait(&bars.t_free[(c - 1) & 1], (c - 1) >> 1);
             if (group_sync_any(group, !ok)) break;
-            // T's two operands, rows i, columns j: tiles of T^T times the column's factor, stored
-            // transposed.
-            const int g = lane >> 2;
+            // T's operand in two parts, rows i, columns j: tiles of T^T stored transposed.
+            const uint32_t timg = smem_u32(sm + kOffT);
             {   // rows 32-63, columns 0-31: 16 x 16 per warp
                 const int i0 = 16 * half, j0 = 16 * (wq >> 1);
                 float z[2][4];
                 block_product<32>(smem_u32(tt), smem_u32(X), smem_u32(tt + kMTT), j0, i0, lane, z);
-                const uint32_t at = sw128_offset(32 + i0 + 8 * (lane >> 4) + (lane & 7), j0 + 8 * ((lane >> 3) & 1), 64);
-                const float be0 = in.beta[j0 + g], be1 = in.beta[j0 + g + 8];
-                const float ev0 = -in.ev[j0 + g], ev1 = -in.ev[j0 + g + 8];
-                stmatrix4_trans(smem_u32(sm + kOffT1) + at, pack(z[0][0] * be0, z[0][1] * be0), pack(z[0][2] * be1, z[0][3] * be1),
-                                pack(z[1][0] * be0, z[1][1] * be0), pack(z[1][2] * be1, z[1][3] * be1));
-                stmatrix4_trans(smem_u32(sm + kOffT2) + at, pack(z[0][0] * ev0, z[0][1] * ev0), pack(z[0][2] * ev1, z[0][3] * ev1),
-                                pack(z[1][0] * ev0, z[1][1] * ev0), pack(z[1][2] * ev1, z[1][3] * ev1));
+                const uint32_t at = timg + sw128_offset(32 + i0 + 8 * (lane >> 4) + (lane & 7), j0 + 8 * ((lane >> 3) & 1), 64);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) split(-z[u >> 1][2 * (u & 1)], -z[u >> 1][2 * (u & 1) + 1], hi[u], lo[u]);
+                stmatrix4_trans(at, hi[0], hi[1], hi[2], hi[3]);
+                stmatrix4_trans(at + 8192, lo[0], lo[1], lo[2], lo[3]);
             }
-            {   // the diagonal blocks: a block and an operand per warp, eight rows at a time
-                // Tiles of T^T: columns j of the image in blocks of eight, rows i.
-                const uint32_t tw = smem_u32(tt + half * kMTT) + 2 * lane * kLdT;
-                const uint32_t img = smem_u32(sm + (is_p ? kOffT2 : kOffT1));
-                float fac[4];
+            // The diagonal blocks: half a block per warp, eight rows i at a time; tiles of T^T are
+            // columns j of the image in blocks of eight.
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = (is_p ? 16 : 0) + 8 * u;
+                const uint32_t tw = smem_u32(tt + half * kMTT) + 2 * (lane * kLdT + i);
+                uint32_t p[4], q[4];
+                ldmatrix4<false>(tw, p);
+                ldmatrix4<false>(tw + kMLow, q);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const int col = 32 * half + 8 * m + g;
-                    fac[m] = is_p ? in.ev[col] : -in.beta[col];
+                    const float2 x = __half22float2(*(const __half2 *)&p[m]), y = __half22float2(*(const __half2 *)&q[m]);
+                    const float2 t = 8 * m <= i ? __fadd2_rn(x, y) : make_float2(0.f, 0.f);
+                    split(t.x, t.y, p[m], q[m]);
                 }
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t p[4];
-                    ldmatrix4<false>(tw + 2 * i, p);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const float2 x = __half22float2(*(const __half2 *)&p[m]);
-                        p[m] = 8 * m <= i ? pack(x.x * fac[m], x.y * fac[m]) : 0u;
-                    }
-                    stmatrix4_trans(img + sw128_offset(32 * half + i + (lane & 7), 32 * half + 8 * (lane >> 3), 64),
-                                    p[0], p[1], p[2], p[3]);
-                }
-            }
-            if (in.len < kC) {
-                // Rows past the last token (another sequence's, or unwritten ones) become zeros
-                // in K and V: T's zeros do not undo an infinity or a NaN.
-                ok = ok && wait(&bars.kq_full[c & 1], c >> 1) && wait(&bars.v_full[c & 1], c >> 1);
-                uint8_t *kt = sm + (c & 1) * kKQStage, *vt = sm + kOffV + (c & 1) * kVStage;
-#pragma unroll 1
-                for (int e = it; e < (kC - in.len) * 8; e += kGroupThreads) {
-                    const uint32_t at = (uint32_t)(in.len + (e >> 3)) * 128u + (uint32_t)(e & 7) * 16u;
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    *(uint4 *)(kt + at) = zero;
-                    *(uint4 *)(kt + 16384 + at) = zero;
-                    *(uint4 *)(vt + at) = zero;
-                    *(uint4 *)(vt + 8192 + at) = zero;
-                }
+                const uint32_t at = timg + sw128_offset(32 * half + i + (lane & 7), 32 * half + 8 * (lane >> 3), 64);
+                stmatrix4_trans(at, p[0], p[1], p[2], p[3]);
+                stmatrix4_trans(at + 8192, q[0], q[1], q[2], q[3]);
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars.t_ready);
@@ -581,15 +647,16 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     } else if (warp < kIssueWarp) {
         // --------------------------------------------------------------- aux --
-        const int wq = warp & 3, it = 32 * wq + lane;
+        const int wq = warp & 3;
         uint8_t *ost = sm + kOffO + 1024 * wq;     // a tile of [16 tokens][32 channels]
         __nv_bfloat16 *o = (__nv_bfloat16 *)a.o;
         const uint32_t osa = smem_u32(ost) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
-        uint32_t xa[32], xb[32];
-        auto output = [&](int c) {
-            const Info &in = infos[c % kInfos];
-            if (!wait(&bars.o_full[stage], phase)) return false;
+#pragma unroll 1
+        for (int c = 0;; ++c) {
+            if (!wait_info(c) || !wait(&bars.o_full[stage], phase)) break;
             next_stage();
+            const Info &in = infos[c % kInfos];
+            const bool last = in.last != 0;
             tc_fence_after_sync();
             // 16 tokens at a time: four 8 x 8 blocks (channels x tokens) become eight token rows of 32
             // channels, 16-byte pieces swizzled by token pair; a lane then stores two of them.
@@ -620,130 +687,69 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tc_fence_before_sync();
             mbar_arrive(&bars.o_free);
-            return true;
-        };
-        bool ok = true;
-#pragma unroll 1
-        for (int c = 0; ok; ++c) {
-            const bool chunk = c == 0 || !infos[(c - 1) % kInfos].last;
-            if (chunk) {
-                ok = wait_info(c);
-                if (!ok) break;
-            // W^T (negated) of key channel 32 wq + lane: 64 tokens -> one 128-byte row.
-            ok = ok && wait(&bars.w_full[c & 1], c >> 1);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (c > 0) ok = wait(&bars.f_full, c - 1);   // the image: read by chunk c - 1's product
-            if (!ok) break;
-            tmem_ld32(tmem_addr(tb, lq, kTW), xa);
-            tmem_ld32(tmem_addr(tb, lq, kTW + 32), xb);
-            tmem_ld_wait();
-            tc_fence_before_sync();
-            mbar_arrive(&bars.w_tfree);
-            auto piece = [&](const uint32_t *x, int col) {
-                *(uint4 *)(sm + kOffW + sw128_offset(it, col, 128)) =
-                    make_uint4(pack(__uint_as_float(x[0]), __uint_as_float(x[1])), pack(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                               pack(__uint_as_float(x[4]), __uint_as_float(x[5])), pack(__uint_as_float(x[6]), __uint_as_float(x[7])));
-            };
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { piece(xa + 8 * i, 8 * i); piece(xb + 8 * i, 32 + 8 * i); }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars.w_ready);
-            }
-            if (c > 0) ok = output(c - 1);
-            if (!chunk) break;
+            if (last) break;
         }
     } else {
     if (warp == kIssueWarp) {
         // ------------------------------------------------------------- issue --
         const bool leader = elect_one();
         const uint32_t id64 = idesc_bf16_f32(128, 64), id128 = idesc_bf16_f32(128, 128);
-        const uint64_t dW = desc_mnmajor_sw128(smem_u32(sm + kOffW), 16384);
-        const uint64_t dT = desc_kmajor_sw128(smem_u32(sm + kOffT2));
-        const uint32_t sb = tmem_addr(tb, 0, kTSb), fb = tmem_addr(tb, 0, kTFb);
-        bool ok = true, more = true;
-#pragma unroll 1
-        for (int c = -1; ok; ++c) {
-            if (c >= 0) {
-                const int s = c & 1;
-                const uint32_t st = smem_u32(sm + s * kKQStage);
-                const uint64_t dQ = desc_kmajor_sw128(st + 8192), dK = desc_mnmajor_sw128(st, 16384);
-                const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + stage * 8192));
-                ok = wait(&bars.kq_full[s], c >> 1) && wait(&bars.w_ready, c) && wait(&bars.s_ready, c);
-                if (!ok) break;
-                tc_fence_after_sync();
-                if (leader) {   // [F^T] += S^T (-W)^T
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem_addr(tb, 0, kTF), sb + 8 * ks, dW + ks * (2048 >> 4), id64 | kIdescMnB, true);
-                    mma_commit(&bars.f_full);
-                }
-                __syncwarp();
-                if (c > 0 && !wait(&bars.o_free, c - 1)) break;
-                tc_fence_after_sync();
-                if (leader) {   // [O^T] = S^T Q^T
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(tmem_addr(tb, 0, kTO), sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
-                }
-                __syncwarp();
-                ok = wait(&bars.f_ready, c);
-                if (!ok) break;
-                tc_fence_after_sync();
-                if (leader) {   // [S^T] += F^T K;  [O^T] += F^T P^T
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(tmem_addr(tb, 0, kTS), fb + 8 * ks, dK + ks * (2048 >> 4), id128 | kIdescMnB, true);
-                    mma_commit(&bars.s_full);
-                    mma_commit(&bars.kq_empty[s]);
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(tmem_addr(tb, 0, kTO), fb + 8 * ks, dP + ks * (32 >> 4), id64, true);
-                    mma_commit(&bars.o_full[stage]);
-                }
-                __syncwarp();
-                more = !infos[c % kInfos].last;
-                next_stage();
-            }
-            if (!more) break;
-            // [F^T] = V^T (T Diag(beta e^{-G}))^T of the next chunk.
-            const int d = c + 1;
-            ok = wait_info(d) && wait(&bars.v_full[d & 1], d >> 1) && wait(&bars.t_ready, d);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (leader) {
-                const uint64_t dv = desc_mnmajor_sw128(smem_u32(sm + kOffV + (d % kVStages) * kVStage), 8192);
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(tmem_addr(tb, 0, kTF), dv + ks * (2048 >> 4), dT + ks * (32 >> 4), id64 | kIdescMnA, ks > 0);
-                mma_commit(&bars.v_empty[d & 1]);
-            }
-            __syncwarp();
-        }
-        if (leader) {
-            mma_commit(&bars.drain[1]);
-            mbar_wait(&bars.drain[1], 0, globaltimer_ns() + kDrainNs);
-        }
-        __syncwarp();
-    } else if (warp == kIssue2Warp) {
-        // ---------------------------------------------------------- issue: W --
-        const bool leader = elect_one();
-        const uint64_t dT = desc_kmajor_sw128(smem_u32(sm + kOffT1));
+        const uint64_t dT = desc_kmajor_sw128(smem_u32(sm + kOffT));
+        const uint32_t sb = tmem_addr(tb, 0, kTSb), rf = tmem_addr(tb, 0, kTRF);
+        const uint32_t tdf = tmem_addr(tb, 0, kTDF), to = tmem_addr(tb, 0, kTO);
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; ok; ++c) {
-            ok = wait(&bars.kq_full[c & 1], c >> 1) && wait(&bars.t_ready, c) && (c == 0 || wait(&bars.w_tfree, c - 1));
+            const int s = c & 1;
+            const uint32_t st = smem_u32(sm + s * kKQStage);
+            const uint64_t dK = desc_kmajor_sw128(st), dQ = desc_kmajor_sw128(st + 8192);
+            const uint64_t dKn = desc_mnmajor_sw128(st, 16384);
+            const uint64_t dP = desc_kmajor_sw128(smem_u32(sm + kOffP + stage * 8192));
+            ok = wait_info(c) && wait(&bars.kq_full[s], c >> 1) && wait(&bars.s_ready, c);
             if (!ok) break;
             tc_fence_after_sync();
-            if (leader) {   // [W^T] = K^T (-T Diag(beta))^T
-                const uint64_t dK = desc_mnmajor_sw128(smem_u32(sm + (c & 1) * kKQStage), 16384);
+            if (leader) {   // [DF] = S^T K^T
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(tmem_addr(tb, 0, kTW), dK + ks * (2048 >> 4), dT + ks * (32 >> 4),
-                           idesc_bf16_f32(128, 64) | kIdescMnA, ks > 0);
-                mma_commit(&bars.w_full[c & 1]);
+                for (int ks = 0; ks < 16; ++ks)
+                    mma_ts(tdf, sb + 8 * ks, dK + ((((ks >> 2) & 1) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
+                mma_commit(&bars.d_full);
             }
             __syncwarp();
+            if (c > 0 && !wait(&bars.o_free, c - 1)) break;
+            tc_fence_after_sync();
+            if (leader) {   // [O^T] = S^T Q^T
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(to, sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
+            }
+            __syncwarp();
+            ok = wait(&bars.t_ready, c) && wait(&bars.r_ready, c);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (leader) {   // [DF] = R^T T^T: high x low, low x high, high x high
+#pragma unroll
+                for (int ks = 0; ks < 12; ++ks)
+                    mma_ts(tdf, rf + 8 * (ks & 3) + (ks >= 4 && ks < 8 ? 32 : 0),
+                           dT + (((ks < 4 ? 8192 : 0) + (ks & 3) * 32) >> 4), id64, ks > 0);
+                mma_commit(&bars.f_full);
+                mma_commit(&bars.t_free[s]);
+            }
+            __syncwarp();
+            ok = wait(&bars.f_ready, c);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (leader) {   // [S^T] += F^T K;  [O^T] += F^T P^T
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(tmem_addr(tb, 0, kTS), rf + 8 * ks, dKn + (ks & 3) * (2048 >> 4), id128 | kIdescMnB, true);
+                mma_commit(&bars.s_full);
+                mma_commit(&bars.kq_empty[s]);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ts(to, rf + 8 * ks, dP + ks * (32 >> 4), id64, true);
+                mma_commit(&bars.o_full[stage]);
+            }
+            __syncwarp();
+            next_stage();
             if (infos[c % kInfos].last) break;
         }
         if (leader) {   // every product of this role has finished before the CTA may exit
@@ -787,35 +793,37 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fetch(start + kC, gn, bn);
             int m = min(kC, len - start);
             m = min(m, to_block);
-            const float x0 = g[0] * kLog2e, x1 = g[1] * kLog2e;
-            const float first = __shfl_sync(0xffffffffu, x0, 0);   // applied to the incoming state
-            const float own = lane == 0 ? x1 : x0 + x1;
-            float sum = own;
+            // The scan is in 64 bits: near its end a chunk's G is large and its differences are not.
+            const double x0 = (double)g[0] * kLog2e, x1 = (double)g[1] * kLog2e;
+            const double first = __shfl_sync(0xffffffffu, x0, 0);   // applied to the incoming state
+            double sum = lane == 0 ? x1 : x0 + x1;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, sum, d);
+                const double y = __shfl_up_sync(0xffffffffu, sum, d);
                 if (lane >= d) sum += y;
             }
-            const float before = __shfl_up_sync(0xffffffffu, sum, 1);
-            const float G0 = lane == 0 ? 0.f : before + x0, G1 = sum;
+            const double before = __shfl_up_sync(0xffffffffu, sum, 1);
+            const double G0 = lane == 0 ? 0. : before + x0, G1 = sum;
             // (A positive log-decay: G need not fall, so it stays within kSafe either way.)
-            const float range = __any_sync(0xffffffffu, x0 > 0.f || x1 > 0.f) ? kSafe : kRange;
-            const uint32_t out0 = __ballot_sync(0xffffffffu, !(fabsf(G0) <= range));
-            const uint32_t out1 = __ballot_sync(0xffffffffu, !(fabsf(G1) <= range));
+            const double range = __any_sync(0xffffffffu, g[0] > 0.f || g[1] > 0.f) ? kSafe : kRange;
+            const uint32_t out0 = __ballot_sync(0xffffffffu, !(fabs(G0) <= range));
+            const uint32_t out1 = __ballot_sync(0xffffffffu, !(fabs(G1) <= range));
             if (out0) m = min(m, 2 * (__ffs(out0) - 1));
             if (out1) m = min(m, 2 * (__ffs(out1) - 1) + 1);
-            const float GC = __shfl_sync(0xffffffffu, (m - 1) & 1 ? G1 : G0, (m - 1) >> 1);
-            const float shift = fmaxf(0.f, -GC - kSafe);
+            const double GC = __shfl_sync(0xffffffffu, (m - 1) & 1 ? G1 : G0, (m - 1) >> 1);
+            const double shift = fmax(0., -GC - kSafe);
             const bool in0 = 2 * lane < m, in1 = 2 * lane + 1 < m;
             Info &in = infos[c % kInfos];
             *(float2 *)&in.beta[2 * lane] = make_float2(in0 ? be[0] : 0.f, in1 ? be[1] : 0.f);
-            *(float2 *)&in.ev[2 * lane] = make_float2(in0 ? be[0] * ex2(-G0 - shift) : 0.f,
-                                                      in1 ? be[1] * ex2(-G1 - shift) : 0.f);
-            *(float2 *)&in.eo[2 * lane] = make_float2(in0 ? a.scale * ex2(G0 + shift) : 0.f,
-                                                      in1 ? a.scale * ex2(G1 + shift) : 0.f);
+            *(float2 *)&in.ev[2 * lane] = make_float2(in0 ? be[0] * pow2(-G0 - shift) : 0.f,
+                                                      in1 ? be[1] * pow2(-G1 - shift) : 0.f);
+            *(float2 *)&in.eo[2 * lane] = make_float2(in0 ? a.scale * pow2(G0 + shift) : 0.f,
+                                                      in1 ? a.scale * pow2(G1 + shift) : 0.f);
+            // The state's two factors multiply it again and again: to the last bit.
+            const float factor = (float)exp2(lane == 0 ? first - shift : GC + shift);
+            if (lane == 1) in.out = factor;
             if (lane == 0) {
-                in.in = ex2(first - shift);
-                in.out = ex2(GC + shift);
+                in.in = factor;
                 in.start = start;
                 in.len = m;
                 in.last = start + m >= len;
@@ -865,8 +873,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (leader) {   // tiles landed and products finished before the CTA may exit
             if (loaded > 0) mbar_wait(&bars.early_full, (loaded - 1) & 1, globaltimer_ns() + kDrainNs);
-            mma_commit(&bars.drain[2]);
-            mbar_wait(&bars.drain[2], 0, globaltimer_ns() + kDrainNs);
+            mma_commit(&bars.drain[1]);
+            mbar_wait(&bars.drain[1], 0, globaltimer_ns() + kDrainNs);
         }
         __syncwarp();
     } else {
