@@ -25,18 +25,19 @@
 // where single bf16 operands gave 2.5e-3.  The outputs' own products take the high parts
 // alone, which their rounding to bf16 hides.
 //
-// One CTA of 23 warps owns a (sequence, value head) and walks its chunks with the fp32 state
+// One CTA of 32 warps owns a (sequence, value head) and walks its chunks with the fp32 state
 // transposed in tensor memory.  Nothing goes through HBM but q, k, v, g, beta, o and the
 // state rows.  Roles:
-//   chain (warps 0-7)    S^T K^T to R^T, F^T, and S^T times its factor, each from its
+//   chain (warps 0-15)   S^T K^T to R^T, F^T, and S^T times its factor, each from its
 //                        accumulator to two bf16 operands; the fp32 master;
-//   intra (warps 8-15)   two groups, even and odd chunks: A and P from the accumulator,
+//   intra (warps 16-23)  two groups, even and odd chunks: A and P from the accumulator,
 //                        T by 16 x 16 forward substitution (fp32) and two block doublings
 //                        (warp products of split fp16), T's two bf16 operands;
-//   aux   (warps 16-19)  O^T to o;
-//   issue (warp 20)      the products of the state chain;
-//   load  (warps 21, 22) chunk bounds and factors (a warp scan), the K and Q tiles for A and P
-//                        and their product; K, Q and V for the chain.
+//   aux   (warps 24-27)  O^T to o;
+//   issue (warp 28)      the products of the state chain;
+//   load  (warps 29, 30) the K and Q tiles for A and P and their product; K, Q and V for the
+//                        chain;
+//   info  (warp 31)      chunk bounds and factors (a warp scan).
 // K and Q are loaded twice (the second time from L2): A and P are formed up to three chunks
 // ahead of the state, and a tile that stayed for both uses would sit idle in between.
 // Products (TMEM accumulators in brackets), chunk c:
@@ -64,12 +65,11 @@ constexpr int kD = 128, kC = 64;              // head size, chunk
 // take microseconds.
 constexpr uint32_t kTries = 1u << 20, kSuspendNs = 2000;
 constexpr uint64_t kDrainNs = 2000000000ull;   // limit of the waits at the end of a role
-constexpr double kLog2e = 1.4426950408889634;
-constexpr double kRange = 200., kSafe = 100.;   // log2 bounds of e^{-G}, see above
+constexpr int64_t kRange = 200ll << 32, kSafe = 100ll << 32;   // log2 bounds of e^{-G}, fixed point
 
-constexpr int kChainThreads = 256, kGroupThreads = 128, kAuxThreads = 128;
-constexpr int kIntraWarp = 8, kAuxWarp = 16, kIssueWarp = 20, kLoadWarp = 21, kLoad2Warp = 22;
-constexpr int kThreads = (kLoad2Warp + 1) * 32;
+constexpr int kChainThreads = 512, kGroupThreads = 128, kAuxThreads = 128;
+constexpr int kIntraWarp = 16, kAuxWarp = 24, kIssueWarp = 28, kLoadWarp = 29, kLoad2Warp = 30, kInfoWarp = 31;
+constexpr int kThreads = (kInfoWarp + 1) * 32;
 
 // Shared memory (offsets from a 1024-aligned base).  A K/Q stage is
 // [k K0 | q K0 | k K1 | q K1], 8 KiB each (64 rows x 128 B, 128-byte swizzle): the
@@ -100,7 +100,7 @@ constexpr uint32_t kTO = 384;    // O^T accumulator
 constexpr uint32_t kTAP = 448;   // A and P accumulators (rows 0-63, 64-127)
 
 struct Bars {
-    uint64_t early_full, kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos];
+    uint64_t early_full, kq_full[kKQStages], kq_empty[kKQStages], info_full[kInfos], info_free[kInfos];
     uint64_t v_full[kVStages], v_empty[kVStages];
     uint64_t ap_full[2], o_full[kPBufs], t_free[2];
     uint64_t ap_tfree, t_ready;
@@ -109,8 +109,7 @@ struct Bars {
 };
 
 // Bounds and factors of a chunk.  Ring slots are reused after kInfos chunks: chunk c's is written
-// after A and P of chunk c - 2 are formed, so those of chunk c - 3 have been read, which waits
-// for the outputs of chunk c - 6; every read of chunk c - 8's comes before those are.
+// once the outputs of chunk c - 6 are out, for which every role is past chunk c - 8.
 struct __align__(16) Info {
     float beta[kC];   // 0 past the chunk's last token
     float ev[kC];     // beta e^{-G}
@@ -133,14 +132,24 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 2^x for |x| up to kSafe and 1, its argument's whole part taken off in 64 bits.
-__device__ __forceinline__ float pow2(double x) {
-    const double n = rint(x);
-    return ex2((float)(x - n)) * __int_as_float(((int)n + 127) << 23);
+// g / ln 2 in fixed point, 32 bits behind the point, clamped far outside any fp32 exponent.
+__device__ __forceinline__ int64_t fixed_log2(float g) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;   // 1 / ln 2
+    g = fminf(fmaxf(g, -4096.f), 4096.f);                      // (NaN becomes -4096: see `bad`)
+    const float p = g * kHi;
+    return __float2ll_rn(p * 0x1p32f) + __float2ll_rn(fmaf(g, kLo, fmaf(g, kHi, -p)) * 0x1p32f);
+}
+// 2^x for a fixed-point x within fp32's exponents.
+__device__ __forceinline__ float pow2(int64_t x) {
+    return ex2((float)(uint32_t)x * 0x1p-32f) * __int_as_float(((int)(x >> 32) + 127) << 23);
 }
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
+}
+// 16 fp32 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&x)[16]) {
+    tmem_st16(taddr, reinterpret_cast<const uint32_t (&)[16]>(x));
 }
 // 16 lanes x 16 columns of TMEM as two 16 x 8 accumulator tiles: r[4 j ..] holds, of column
 // group 8 j, (lane g, columns 2t, 2t + 1) and (lane g + 8, the same columns), with
@@ -324,7 +333,10 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(&bars.early_full, 1);
         for (int s = 0; s < 2; ++s) mbar_init(&bars.drain[s], 1);
         for (int s = 0; s < kPBufs; ++s) mbar_init(&bars.o_full[s], 1);
-        for (int s = 0; s < kInfos; ++s) mbar_init(&bars.info_full[s], 1);
+        for (int s = 0; s < kInfos; ++s) {
+            mbar_init(&bars.info_full[s], 1);
+            mbar_init(&bars.info_free[s], kAuxThreads);
+        }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], kChainThreads);
@@ -373,15 +385,20 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (warp < kIntraWarp) {
         // ------------------------------------------------------------- chain --
-        const int j = tid & 127, hh = warp >> 2;   // value channel; half of tokens / key channels
-        const float *S0 = src >= 0 ? row_of(src) + (size_t)(64 * hh) * kD + j : nullptr;
-        // 32 columns of an accumulator as two bf16 operands of 16 columns each.
-        auto put = [&](const uint32_t (&x)[32], uint32_t hi, uint32_t lo) {
-            uint32_t h[16], l[16];
+        const int j = tid & 127, hh = warp >> 2;   // value channel; quarter of tokens / key channels
+        const float *S0 = src >= 0 ? row_of(src) + (size_t)(32 * hh) * kD + j : nullptr;
+        // 16 columns of an accumulator as two bf16 operands of 8 columns each.
+        auto put16 = [&](const float (&x)[16], uint32_t hi, uint32_t lo) {
+            float h[8], l[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) split(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), h[i], l[i]);
-            tmem_st16(tmem_addr(tb, lq, hi), h);
-            tmem_st16(tmem_addr(tb, lq, lo), l);
+            for (int i = 0; i < 8; ++i) {
+                uint32_t a, b;
+                split(x[2 * i], x[2 * i + 1], a, b);
+                h[i] = __uint_as_float(a);
+                l[i] = __uint_as_float(b);
+            }
+            tmem_st8(tmem_addr(tb, lq, hi), h);
+            tmem_st8(tmem_addr(tb, lq, lo), l);
         };
         auto hand_over = [&](uint64_t *bar) {
             tmem_st_wait();
@@ -391,31 +408,31 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         bool ok = wait_info(0);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
-            uint32_t x[32];
+            float x[16];
             const float f = infos[0].in;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                x[i] = S0 ? __float_as_uint(S0[(size_t)(32 * p + i) * kD] * f) : 0u;
-            tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
-            put(x, kTSb + 32 * hh + 16 * p, kTSb + 64 + 32 * hh + 16 * p);
+            for (int i = 0; i < 16; ++i) x[i] = S0 ? S0[(size_t)(16 * p + i) * kD] * f : 0.f;
+            tmem_st16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
+            put16(x, kTSb + 16 * hh + 8 * p, kTSb + 64 + 16 * hh + 8 * p);
         }
         hand_over(&bars.s_ready);
 #pragma unroll 1
         for (int c = 0; ok; ++c) {
-            uint32_t x[32];
+            float x[16];
             const Info &in = infos[c % kInfos];
             const bool last = in.last != 0;
             const float out = in.out;
-            // V of this thread's channel and half of the tokens, packed by pairs.
+            // V of this thread's channel and quarter of the tokens.
             ok = wait(&bars.v_full[c & 1], c >> 1);
-            uint32_t v[16];
+            float2 w[8];      // beta e^{-G} V^T
             {
-                const uint8_t *vt = sm + kOffV + (c & 1) * kVStage + (j >> 6) * 8192 + 32 * hh * 128;
+                const uint8_t *vt = sm + kOffV + (c & 1) * kVStage + (j >> 6) * 8192 + 16 * hh * 128;
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int i = 0; i < 16; i += 2) {
                     const uint32_t a0 = *(const uint16_t *)(vt + sw128_offset(i, j & 63, 64));
                     const uint32_t a1 = *(const uint16_t *)(vt + sw128_offset(i + 1, j & 63, 64));
-                    v[i / 2] = a0 | (a1 << 16);
+                    w[i / 2] = __fmul2_rn(*(const float2 *)&in.ev[16 * hh + i],
+                                          make_float2(__uint_as_float(a0 << 16), __uint_as_float(a1 << 16)));
                 }
             }
             mbar_arrive(&bars.v_empty[c & 1]);
@@ -433,30 +450,28 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ok = ok && wait(&bars.d_full, c);
             if (!ok) break;
             tc_fence_after_sync();
-            tmem_ld32(tmem_addr(tb, lq, kTDF + 32 * hh), x);
+            tmem_ld16f(tmem_addr(tb, lq, kTDF + 16 * hh), x);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 be = *(const float4 *)&in.beta[32 * hh + i], ev = *(const float4 *)&in.ev[32 * hh + i];
-                const uint32_t v0 = v[i / 2], v1 = v[i / 2 + 1];
-                x[i] = __float_as_uint(fmaf(-be.x, __uint_as_float(x[i]), ev.x * __uint_as_float(v0 << 16)));
-                x[i + 1] = __float_as_uint(fmaf(-be.y, __uint_as_float(x[i + 1]), ev.y * __uint_as_float(v0 & 0xFFFF0000u)));
-                x[i + 2] = __float_as_uint(fmaf(-be.z, __uint_as_float(x[i + 2]), ev.z * __uint_as_float(v1 << 16)));
-                x[i + 3] = __float_as_uint(fmaf(-be.w, __uint_as_float(x[i + 3]), ev.w * __uint_as_float(v1 & 0xFFFF0000u)));
+            for (int i = 0; i < 16; i += 2) {
+                const float2 be = *(const float2 *)&in.beta[16 * hh + i];
+                const float2 t = __ffma2_rn(make_float2(-be.x, -be.y), make_float2(x[i], x[i + 1]), w[i / 2]);
+                x[i] = t.x;
+                x[i + 1] = t.y;
             }
             if (in.len < kC) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = 32 * hh + i < in.len ? x[i] : 0u;
+                for (int i = 0; i < 16; ++i) x[i] = 16 * hh + i < in.len ? x[i] : 0.f;
             }
-            put(x, kTRF + 16 * hh, kTRF + 32 + 16 * hh);
+            put16(x, kTRF + 8 * hh, kTRF + 32 + 8 * hh);
             hand_over(&bars.r_ready);
             // F^T = R^T T^T.
             ok = wait(&bars.f_full, c);
             if (!ok) break;
             tc_fence_after_sync();
-            tmem_ld32(tmem_addr(tb, lq, kTDF + 32 * hh), x);
+            tmem_ld16f(tmem_addr(tb, lq, kTDF + 16 * hh), x);
             tmem_ld_wait();
-            put(x, kTRF + 16 * hh, kTRF + 32 + 16 * hh);
+            put16(x, kTRF + 8 * hh, kTRF + 32 + 8 * hh);
             hand_over(&bars.f_ready);
             const int row = in.row;
             if (!last) ok = wait_info(c + 1);
@@ -469,27 +484,26 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int w = 0; w < 4; ++w) {
                     const int to = w < 2 ? row : (last ? dst : -1), p = w & 1;
                     if (to < 0) continue;
-                    tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
+                    tmem_ld16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
                     tmem_ld_wait();
-                    float *Sf = row_of(to) + (size_t)(64 * hh + 32 * p) * kD + j;
+                    float *Sf = row_of(to) + (size_t)(32 * hh + 16 * p) * kD + j;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) Sf[(size_t)i * kD] = __uint_as_float(x[i]) * out;
+                    for (int i = 0; i < 16; ++i) Sf[(size_t)i * kD] = x[i] * out;
                 }
                 if (last) break;
             }
-#pragma unroll 1
+#pragma unroll
             for (int p = 0; p < 2; ++p) {
-                tmem_ld32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
+                tmem_ld16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 t = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                                make_float2(f, f));
-                    x[i] = __float_as_uint(t.x);
-                    x[i + 1] = __float_as_uint(t.y);
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 t = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(f, f));
+                    x[i] = t.x;
+                    x[i + 1] = t.y;
                 }
-                tmem_st32(tmem_addr(tb, lq, kTS + 64 * hh + 32 * p), x);
-                put(x, kTSb + 32 * hh + 16 * p, kTSb + 64 + 32 * hh + 16 * p);
+                tmem_st16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
+                put16(x, kTSb + 16 * hh + 8 * p, kTSb + 64 + 16 * hh + 8 * p);
             }
             hand_over(&bars.s_ready);
         }
@@ -687,6 +701,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             tc_fence_before_sync();
             mbar_arrive(&bars.o_free);
+            mbar_arrive(&bars.info_free[c % kInfos]);
             if (last) break;
         }
     } else {
@@ -715,14 +730,6 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mma_commit(&bars.d_full);
             }
             __syncwarp();
-            if (c > 0 && !wait(&bars.o_free, c - 1)) break;
-            tc_fence_after_sync();
-            if (leader) {   // [O^T] = S^T Q^T
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(to, sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
-            }
-            __syncwarp();
             ok = wait(&bars.t_ready, c) && wait(&bars.r_ready, c);
             if (!ok) break;
             tc_fence_after_sync();
@@ -733,6 +740,14 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                            dT + (((ks < 4 ? 8192 : 0) + (ks & 3) * 32) >> 4), id64, ks > 0);
                 mma_commit(&bars.f_full);
                 mma_commit(&bars.t_free[s]);
+            }
+            __syncwarp();
+            if (c > 0 && !wait(&bars.o_free, c - 1)) break;
+            tc_fence_after_sync();
+            if (leader) {   // [O^T] = S^T Q^T
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(to, sb + 8 * ks, dQ + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), id64, ks > 0);
             }
             __syncwarp();
             ok = wait(&bars.f_ready, c);
@@ -760,21 +775,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == kLoadWarp) {
         // -------------------------------------------------------------- load --
         const bool leader = elect_one();
-        int start = 0, loaded = 0;
-        // Tokens left in the current block, and its index (no blocks: more than there are).
-        int to_block = a.block > 0 ? a.block - ctx % a.block : 0x7fffffff, blk = a.block > 0 ? ctx / a.block : 0;
-        // g and beta of tokens 2 lane, 2 lane + 1 of this chunk, and of the next if this one is full.
-        float g[2], be[2], gn[2], bn[2];
-        auto fetch = [&](int from, float (&g)[2], float (&be)[2]) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = from + 2 * lane + u;
-                const size_t x = (size_t)(tbeg + t) * a.H + h;
-                g[u] = t < len ? a.g[x] : 0.f;
-                be[u] = t < len ? a.beta[x] : 0.f;
-            }
-        };
-        // The tiles of tokens t0 .. t0 + 63 into L2, two chunks ahead of their loads.
+        int loaded = 0;
+        // The tiles of tokens t .. t + 63 into L2, a chunk ahead of their loads.
         auto prefetch = [&](int t) {
             if (!leader || t >= len) return;
             for (int x = 0; x < kD; x += 64) {
@@ -783,58 +785,13 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tma_prefetch(&tm_v, x, h, tbeg + t);
             }
         };
-        fetch(0, g, be);
         prefetch(kC);
-        bool ok = true;
 #pragma unroll 1
-        for (int c = 0; ok && start < len; ++c) {
-            // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row, and the
-            // range of e^{-G}; then the factors.
-            fetch(start + kC, gn, bn);
-            int m = min(kC, len - start);
-            m = min(m, to_block);
-            // The scan is in 64 bits: near its end a chunk's G is large and its differences are not.
-            const double x0 = (double)g[0] * kLog2e, x1 = (double)g[1] * kLog2e;
-            const double first = __shfl_sync(0xffffffffu, x0, 0);   // applied to the incoming state
-            double sum = lane == 0 ? x1 : x0 + x1;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += y;
-            }
-            const double before = __shfl_up_sync(0xffffffffu, sum, 1);
-            const double G0 = lane == 0 ? 0. : before + x0, G1 = sum;
-            // (A positive log-decay: G need not fall, so it stays within kSafe either way.)
-            const double range = __any_sync(0xffffffffu, g[0] > 0.f || g[1] > 0.f) ? kSafe : kRange;
-            const uint32_t out0 = __ballot_sync(0xffffffffu, !(fabs(G0) <= range));
-            const uint32_t out1 = __ballot_sync(0xffffffffu, !(fabs(G1) <= range));
-            if (out0) m = min(m, 2 * (__ffs(out0) - 1));
-            if (out1) m = min(m, 2 * (__ffs(out1) - 1) + 1);
-            const double GC = __shfl_sync(0xffffffffu, (m - 1) & 1 ? G1 : G0, (m - 1) >> 1);
-            const double shift = fmax(0., -GC - kSafe);
-            const bool in0 = 2 * lane < m, in1 = 2 * lane + 1 < m;
-            Info &in = infos[c % kInfos];
-            *(float2 *)&in.beta[2 * lane] = make_float2(in0 ? be[0] : 0.f, in1 ? be[1] : 0.f);
-            *(float2 *)&in.ev[2 * lane] = make_float2(in0 ? be[0] * pow2(-G0 - shift) : 0.f,
-                                                      in1 ? be[1] * pow2(-G1 - shift) : 0.f);
-            *(float2 *)&in.eo[2 * lane] = make_float2(in0 ? a.scale * pow2(G0 + shift) : 0.f,
-                                                      in1 ? a.scale * pow2(G1 + shift) : 0.f);
-            // The state's two factors multiply it again and again: to the last bit.
-            const float factor = (float)exp2(lane == 0 ? first - shift : GC + shift);
-            if (lane == 1) in.out = factor;
-            if (lane == 0) {
-                in.in = factor;
-                in.start = start;
-                in.len = m;
-                in.last = start + m >= len;
-                in.row = -1;
-                if (a.block > 0 && m == to_block && blk < a.table_cols) {
-                    const int row = a.table[(size_t)n * a.table_cols + blk];
-                    if (row >= 0 && row < a.pool_size) in.row = row;
-                }
-            }
-            __syncwarp();
-            if (leader) mbar_arrive(&bars.info_full[c % kInfos]);
+        for (int c = 0;; ++c) {
+            if (!wait_info(c)) break;
+            const Info &in = infos[c % kInfos];
+            const int start = in.start, next = start + in.len;
+            const bool last = in.last != 0;
             if (c > 0 && !wait(&bars.ap_full[(c - 1) & 1], (c - 1) >> 1)) break;
             if (leader) {
                 uint8_t *st = sm + kOffEarly;
@@ -847,7 +804,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             ++loaded;
             __syncwarp();
-            prefetch(start + m + kC);
+            prefetch(next + kC);
             // [AP] = [K; Q] K^T, once the previous chunk's A and P have been read.
             if (!wait(&bars.early_full, c) || (c > 0 && !wait(&bars.ap_tfree, c - 1))) break;
             tc_fence_after_sync();
@@ -861,15 +818,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mma_commit(&bars.ap_full[c & 1]);
             }
             __syncwarp();
-            start += m;
-            to_block -= m;
-            if (to_block == 0 && a.block > 0) { to_block = a.block; ++blk; }
-            if (m == kC) {
-                g[0] = gn[0]; g[1] = gn[1];
-                be[0] = bn[0]; be[1] = bn[1];
-            } else if (start < len) {
-                fetch(start, g, be);
-            }
+            if (last) break;
         }
         if (leader) {   // tiles landed and products finished before the CTA may exit
             if (loaded > 0) mbar_wait(&bars.early_full, (loaded - 1) & 1, globaltimer_ns() + kDrainNs);
@@ -877,7 +826,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_wait(&bars.drain[1], 0, globaltimer_ns() + kDrainNs);
         }
         __syncwarp();
-    } else {
+    } else if (warp == kLoad2Warp) {
         // ---------------------------------------------- load: the other products --
         const bool leader = elect_one();
         int loaded = 0;
@@ -909,6 +858,88 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_wait(&bars.v_full[c & 1], (c >> 1) & 1, globaltimer_ns() + kDrainNs);
             }
         __syncwarp();
+    } else {
+        // -------------------------------------------------------------- info --
+        int start = 0;
+        // Tokens left in the current block, and its index (no blocks: more than there are).
+        int to_block = a.block > 0 ? a.block - ctx % a.block : 0x7fffffff, blk = a.block > 0 ? ctx / a.block : 0;
+        // g and beta of tokens 2 lane, 2 lane + 1 of this chunk, and of the next if this one is full.
+        float g[2], be[2], gn[2], bn[2];
+        auto fetch = [&](int from, float (&g)[2], float (&be)[2]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = from + 2 * lane + u;
+                const size_t x = (size_t)(tbeg + t) * a.H + h;
+                g[u] = t < len ? a.g[x] : 0.f;
+                be[u] = t < len ? a.beta[x] : 0.f;
+            }
+        };
+        fetch(0, g, be);
+#pragma unroll 1
+        for (int c = 0; start < len; ++c) {
+            if (c >= 6 && !wait(&bars.info_free[(c - 6) % kInfos], (c - 6) / kInfos)) break;
+            // Bounds: 64 tokens, the sequence's end, the end of a block that wants its row, and the
+            // range of e^{-G}; then the factors.
+            fetch(start + kC, gn, bn);
+            int m = min(kC, len - start);
+            m = min(m, to_block);
+            // The scan is in 64 bits (fixed point, 32 of them behind the point): near its end a
+            // chunk's G is large and its differences are not.
+            const int64_t x0 = fixed_log2(g[0]), x1 = fixed_log2(g[1]);
+            const int64_t first = __shfl_sync(0xffffffffu, x0, 0);   // applied to the incoming state
+            int64_t sum = lane == 0 ? x1 : x0 + x1;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += y;
+            }
+            const int64_t before = __shfl_up_sync(0xffffffffu, sum, 1);
+            const int64_t G0 = lane == 0 ? 0 : before + x0, G1 = sum;
+            // (A positive log-decay: G need not fall, so it stays within kSafe either way.)
+            const int64_t range = __any_sync(0xffffffffu, !(g[0] <= 0.f) || !(g[1] <= 0.f)) ? kSafe : kRange;
+            const uint32_t out0 = __ballot_sync(0xffffffffu, G0 > range || G0 < -range);
+            const uint32_t out1 = __ballot_sync(0xffffffffu, G1 > range || G1 < -range);
+            if (out0) m = min(m, 2 * (__ffs(out0) - 1));
+            if (out1) m = min(m, 2 * (__ffs(out1) - 1) + 1);
+            const int64_t GC = __shfl_sync(0xffffffffu, (m - 1) & 1 ? G1 : G0, (m - 1) >> 1);
+            const int64_t shift = max((int64_t)0, -GC - kSafe);
+            const bool in0 = 2 * lane < m, in1 = 2 * lane + 1 < m;
+            // A NaN among the log-decays reaches its token's factors, and the state's.
+            const float bad0 = g[0] == g[0] ? 0.f : g[0], bad1 = g[1] == g[1] ? 0.f : g[1];
+            Info &in = infos[c % kInfos];
+            *(float2 *)&in.beta[2 * lane] = make_float2(in0 ? be[0] : 0.f, in1 ? be[1] : 0.f);
+            *(float2 *)&in.ev[2 * lane] = make_float2(in0 ? be[0] * pow2(-G0 - shift) + bad0 : 0.f,
+                                                      in1 ? be[1] * pow2(-G1 - shift) + bad1 : 0.f);
+            *(float2 *)&in.eo[2 * lane] = make_float2(in0 ? a.scale * pow2(G0 + shift) + bad0 : 0.f,
+                                                      in1 ? a.scale * pow2(G1 + shift) + bad1 : 0.f);
+            const float bad = __uint_as_float(__reduce_or_sync(
+                0xffffffffu, (in0 ? __float_as_uint(bad0) : 0u) | (in1 ? __float_as_uint(bad1) : 0u)));
+            // The state's two factors multiply it again and again: to the last bit.
+            const float factor = (float)exp2((double)(lane == 0 ? first - shift : GC + shift) * 0x1p-32) + bad;
+            if (lane == 1) in.out = factor;
+            if (lane == 0) {
+                in.in = factor;
+                in.start = start;
+                in.len = m;
+                in.last = start + m >= len;
+                in.row = -1;
+                if (a.block > 0 && m == to_block && blk < a.table_cols) {
+                    const int row = a.table[(size_t)n * a.table_cols + blk];
+                    if (row >= 0 && row < a.pool_size) in.row = row;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.info_full[c % kInfos]);
+            start += m;
+            to_block -= m;
+            if (to_block == 0 && a.block > 0) { to_block = a.block; ++blk; }
+            if (m == kC) {
+                g[0] = gn[0]; g[1] = gn[1];
+                be[0] = bn[0]; be[1] = bn[1];
+            } else if (start < len) {
+                fetch(start, g, be);
+            }
+        }
     }
     }
     if (!alive && lane == 0) atomicCAS(a.status, 0, (int32_t)KDA_TC_TIMEOUT_CODE);
