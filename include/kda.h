@@ -501,7 +501,8 @@ kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const flo
  *   block_table     device int32 [num_seqs, block_table_cols], in and out: entries of
  *                   newly reached blocks are written, all others left as they
  *                   were.  An entry that the free list cannot fill is -1;
- *                   blocks past block_table_cols have no entry.
+ *                   blocks past block_table_cols have no entry.  At most 2^31 - 1
+ *                   entries.
  *   cu_seqlens      out [num_seqs + 1]: packed offsets of the new tokens.
  *   positions       out [total_tokens] or NULL: position of each new token in its
  *                   request.  total_tokens is the length of the two buffers; entries

@@ -354,52 +354,52 @@ def kda_decode_check_slots(slots_host, pool_size: int) -> bool:
 
 # ------------------------------------------------- gated delta rule, block plan --
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype, device, shape=None):
-    """Address of a tensor that must be contiguous, of ``dtype`` and on ``device`` (and of
-    ``shape``); None stays None."""
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, index: int, shape=None):
+    """Address of a tensor that must be contiguous, of ``dtype`` and on CUDA device ``index``
+    (and of ``shape``); None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _call(fn, where: str, device, stream, *args):
-    """One library call on ``device``, on ``stream`` or that device's current stream."""
-    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch._C._cuda_getDevice():
+def _call(fn, where: str, index: int, stream, *args):
+    """One library call on device ``index``, on ``stream`` or that device's current stream."""
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
         code = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             code = fn(*args, raw)
     if code != 0:
         raise KdaError(code, where)
 
 
-def _gdr_device(q, k, v):
-    dev = q.device
-    if dev.type != "cuda":
+def _gdr_device(q, k, v) -> int:
+    index = q.get_device()
+    if index < 0:
         raise ValueError("q must be a CUDA tensor")
     if q.dtype not in KDA_DTYPE:
         raise ValueError(f"unsupported dtype {q.dtype}")
     if k.shape != q.shape:
         raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
-    if v.shape[:-2] != q.shape[:-2]:
-        raise ValueError("v must have q's leading dimensions")
-    return dev
+    return index
 
 
-def _pool(state, H, dk, dv, device):
+def _pool(state, H, dk, dv, index: int):
     """Address and rows of the state pool [P, H, dk, dv]."""
     if state is None:
         return None, 0
-    return _ptr(state, "state", torch.float32, device, (state.shape[0], H, dk, dv)), state.shape[0]
+    rows = state.shape[0]
+    return _ptr(state, "state", torch.float32, index, (rows, H, dk, dv)), rows
 
 
 def kda_gdr_prefill_workspace_size(total_tokens: int, num_seqs: int, Hk: int, H: int, dk: int,
@@ -424,14 +424,14 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     """
     dev = _gdr_device(q, k, v)
     T, Hk, dk = q.shape
-    H, dv = v.shape[1:]
+    _, H, dv = v.shape
     N = cu_seqlens.shape[0] - 1
     dt = q.dtype
     if o is None:
         o = torch.empty_like(v)
     need = _lib.kda_gdr_prefill_workspace_size(T, N, Hk, H, dk, dv, KDA_DTYPE[dt], KDA_ALGO[algo])
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     host = None
     if cu_seqlens_host is not None:
         if cu_seqlens_host.numel() != N + 1:
@@ -445,7 +445,7 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     pool, rows = _pool(state, H, dk, dv, dev)
     cols = block_table.shape[1] if block_table is not None else 0
     _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream,
-          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev),
+          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, (T, H, dv)),
           _ptr(g, "g", torch.float32, dev, (T, H)), _ptr(beta, "beta", torch.float32, dev, (T, H)),
           _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev), host, N, T, Hk, H, dk, dv,
           KDA_DTYPE[dt], scale, pool, rows, _ptr(src_slots, "src_slots", torch.int32, dev, (N,)),
@@ -468,22 +468,26 @@ def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_
     ``update_state=False`` is a verify pass.
     """
     dev = _gdr_device(q, k, v)
-    Tq = 1 if q.dim() == 3 else q.shape[1]
-    B, Hk, dk = q.shape[0], q.shape[-2], q.shape[-1]
+    if q.dim() == 3:
+        B, Hk, dk = q.shape
+        Tq, lead = 1, (B,)
+    else:
+        B, Tq, Hk, dk = q.shape
+        lead = (B, Tq)
     H, dv = v.shape[-2:]
-    dt = q.dtype
+    dt, f32, i32 = q.dtype, torch.float32, torch.int32
+    vshape, gshape, slots = (*lead, H, dv), (*lead, H), (B,)
     if o is None and (want_outputs or not update_state):
         o = torch.empty_like(v)
     pool, rows = _pool(state, H, dk, dv, dev)
-    lead = v.shape[:-1]
     _call(_lib.kda_gdr_decode, "kda_gdr_decode", dev, stream,
-          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev),
-          _ptr(g, "g", torch.float32, dev, lead), _ptr(beta, "beta", torch.float32, dev, lead),
+          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, vshape),
+          _ptr(g, "g", f32, dev, gshape), _ptr(beta, "beta", f32, dev, gshape),
           B, Tq, Hk, H, dk, dv, KDA_DTYPE[dt], scale, pool, rows,
-          _ptr(src_slots, "src_slots", torch.int32, dev, (B,)),
-          _ptr(dst_slots, "dst_slots", torch.int32, dev, (B,)),
-          _ptr(num_tokens, "num_tokens", torch.int32, dev, (B,)), 1 if update_state else 0,
-          _ptr(o, "o", dt, dev, v.shape))
+          _ptr(src_slots, "src_slots", i32, dev, slots),
+          _ptr(dst_slots, "dst_slots", i32, dev, slots),
+          _ptr(num_tokens, "num_tokens", i32, dev, slots), 1 if update_state else 0,
+          _ptr(o, "o", dt, dev, vshape))
     return o
 
 
@@ -507,22 +511,22 @@ def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, bloc
     the token outputs (entries past the last token are -1).  Returns a ``BlockPlan``;
     ``out`` passes its tensors (``out.free_head`` may be ``free_head`` itself).
     """
-    dev = new_lens.device
-    if dev.type != "cuda":
+    dev = new_lens.get_device()
+    if dev < 0:
         raise ValueError("new_lens must be a CUDA tensor")
-    N, F = new_lens.shape[0], free_blocks.shape[0]
-    i32 = torch.int32
+    (N,), (F,), i32 = new_lens.shape, free_blocks.shape, torch.int32
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must have shape ({N}, blocks)")
     if total_tokens < 0:
         raise ValueError("total_tokens must not be negative")
     if out is None:
-        # One allocation: the int64 slots first, then every int32 output.
-        buf = torch.empty(12 * total_tokens + 4 * (3 * N + 2), dtype=torch.uint8, device=dev)
-        ints = buf[8 * total_tokens:].view(i32)
-        out = BlockPlan(ints[:N + 1], ints[3 * N + 2:], buf[:8 * total_tokens].view(torch.int64),
-                        ints[N + 1:2 * N + 1], ints[2 * N + 1:3 * N + 1],
-                        ints[3 * N + 1:3 * N + 2])
+        # One allocation for the int32 outputs, padded so that the positions are 16-byte aligned.
+        pad = -(3 * N + 2) % 4
+        cu, src, dst, head, _, pos = torch.empty(
+            3 * N + 2 + pad + total_tokens, dtype=i32, device=new_lens.device).split_with_sizes(
+                (N + 1, N, N, 1, pad, total_tokens))
+        out = BlockPlan(cu, pos, torch.empty(total_tokens, dtype=torch.int64, device=new_lens.device),
+                        src, dst, head)
     _call(_lib.kda_block_plan, "kda_block_plan", dev, stream,
           _ptr(new_lens, "new_lens", i32, dev, (N,)), _ptr(ctx_lens, "ctx_lens", i32, dev, (N,)),
           N, _ptr(free_blocks, "free_blocks", i32, dev, (F,)), F,

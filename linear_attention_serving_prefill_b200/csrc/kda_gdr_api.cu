@@ -154,6 +154,7 @@ extern "C" kda_status kda_block_plan(const int32_t *new_lens, const int32_t *ctx
     if (num_seqs > 0 && (!new_lens || !block_table || block_table_cols == 0))
         return KDA_ERR_INVALID_ARG;
     if (num_free > 0 && !free_blocks) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)num_seqs * block_table_cols > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
     for (const void *p : {(const void *)new_lens, (const void *)ctx_lens, (const void *)free_blocks,
                           (const void *)free_head, (const void *)block_table,
                           (const void *)cu_seqlens, (const void *)positions,

@@ -9,12 +9,20 @@
 // (speculative verify and replay).
 //
 // Columns of S never mix, so a warp owns 16 value columns for all dk key
-// channels: lane (rq, c) keeps rows 4 i + rq of the column pair 2 c, 2 c + 1 (64
-// registers at dk = 128), both reductions of a token are two xor shuffles over
-// the four row groups, and no token step crosses warps.  q, k, v, g and beta of
-// kGroup tokens at a time are staged in shared memory as fp32 (k and q permuted
-// so that a lane's rows are contiguous); the next group's global loads are in
-// flight while the current one runs.
+// channels: lane (rq, c) keeps the row pairs 8 i + 2 rq, + 1 of the columns 2 c and
+// 2 c + 1 (64 registers at dk = 128), both reductions of a token are two xor
+// shuffles over the four row groups, and no token step crosses warps.  Packed fp32
+// pairs run along the rows, so that the pairs of k and q come as they lie in
+// shared memory.  The decays are not applied token by token: the registers hold
+// S / run with one running factor run = prod e^{g}, folded in before it leaves
+// [2^-32, 2^32], so a token costs three packed products per row pair and column.
+// q, k, v, g and beta of kGroup tokens at a time are staged in shared memory as
+// fp32; the next group's global loads are in flight while the current one runs.
+//
+// A long sequence is bound by the latency of one token's chain (0.35 us at dk = 128,
+// 0.30 us at dk = 64: two reductions, their shuffles and the update, one after the other);
+// a verify pass of a few tokens by reading the states (64 x 96 states, 4 tokens: 139 us,
+// 3.1 TB/s).
 #include "kda_common.cuh"
 #include "kda_gdr.h"
 
@@ -42,10 +50,10 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
     }
 }
 
-__device__ __forceinline__ float2 shfl_add(float2 x, int mask) {
-    x.x += __shfl_xor_sync(0xffffffffu, x.x, mask);
-    x.y += __shfl_xor_sync(0xffffffffu, x.y, mask);
-    return x;
+// Sum over the four row groups.
+__device__ __forceinline__ float group_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
 // Two fp32 outputs to adjacent storage elements.
@@ -54,14 +62,19 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 x) {
     *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x.x, x.y);
 }
 
-template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(DV >= 64 ? 128 : 64)
+// kMinBlocks: 4 (128 registers, a few of them spilled at dk = 128) holds more states per SM
+// and wins where each sequence has a few tokens and loading the states counts; 1 wins over
+// long sequences.  bf16, dk = dv = 128, 4 / 1: verify of 64 x 4 tokens, 32 heads 139 / 146 us;
+// replay of 256 x up to 8 tokens 265 / 285 us.  dv = 64, prefill of 2048 tokens, 16 heads:
+// 1112 / 836 us.
+template <int DK, int DV, typename T, int kMinBlocks>
+__global__ void __launch_bounds__(DV >= 64 ? 128 : 64, kMinBlocks)
 gdr_recurrent_kernel(GdrArgs a)
 {
     constexpr int kWarps = DV >= 64 ? 4 : 2, kThreads = 32 * kWarps;
     constexpr int kCols = 16 * kWarps;           // value columns of this CTA
-    constexpr int R = DK / 4;                    // rows per lane
-    constexpr int kLd = R + 4;                   // row-group stride: distinct banks for the four groups
+    constexpr int R = DK / 8;                    // row pairs per lane
+    constexpr int kLd = DK / 4 + 4;              // row-group stride: distinct banks for the four groups
     constexpr int kPieces = kGroup * DK / 8;     // 8-element pieces of one staged operand
     constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
     constexpr int kVPieces = kGroup * kCols / 8;
@@ -94,27 +107,47 @@ gdr_recurrent_kernel(GdrArgs a)
     if (!a.state || src < 0 || src >= a.pool_size) src = -1;
     if (!a.state || !a.update || dst < 0 || dst >= a.pool_size) dst = -1;
     if (len == 0 && dst < 0) return;
-    const size_t own = (size_t)rq * DV + col;    // row rq, this lane's column pair
+    const size_t own = (size_t)(2 * rq) * DV + col;    // row 2 rq, this lane's column pair
     auto row_of = [&](int slot) { return a.state + ((size_t)slot * a.H + h) * DK * DV + own; };
 
-    float2 s[R];
-    if (src >= 0) {
-        const float *p = row_of(src);
+    float2 s0[R], s1[R];     // row pairs of columns col and col + 1, over run
+    float run = 1.f;
+    {
+        const float *p = src >= 0 ? row_of(src) : nullptr;
 #pragma unroll
-        for (int i = 0; i < R; ++i) s[i] = *(const float2 *)(p + (size_t)4 * i * DV);
-    } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) s[i] = make_float2(0.f, 0.f);
+        for (int i = 0; i < R; ++i) {
+            float2 x = make_float2(0.f, 0.f), y = x;
+            if (p) {
+                x = *(const float2 *)(p + (size_t)8 * i * DV);
+                y = *(const float2 *)(p + (size_t)(8 * i + 1) * DV);
+            }
+            s0[i] = make_float2(x.x, y.x);
+            s1[i] = make_float2(x.y, y.y);
+        }
     }
+    auto fold = [&] {        // run into the state
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            s0[i] = __fmul2_rn(s0[i], make_float2(run, run));
+            s1[i] = __fmul2_rn(s1[i], make_float2(run, run));
+        }
+        run = 1.f;
+    };
     auto write_row = [&](int slot) {
         float *p = row_of(slot);
 #pragma unroll
-        for (int i = 0; i < R; ++i) *(float2 *)(p + (size_t)4 * i * DV) = s[i];
+        for (int i = 0; i < R; ++i) {
+            *(float2 *)(p + (size_t)8 * i * DV) = make_float2(run * s0[i].x, run * s1[i].x);
+            *(float2 *)(p + (size_t)(8 * i + 1) * DV) = make_float2(run * s0[i].y, run * s1[i].y);
+        }
     };
 
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v;
     T *o = (T *)a.o;
-    const int ctx = a.ctx ? a.ctx[n] : 0;
+    // Tokens left in the current block, and its index (no blocks: more than there are tokens).
+    const int ctx = a.ctx ? max(a.ctx[n], 0) : 0;
+    int64_t to_block = a.block > 0 ? a.block - ctx % a.block : (int64_t)1 << 40;
+    int blk = a.block > 0 ? ctx / a.block : 0;
     float pk[kPer][8], pq[kPer][8], pv[kVPer][8], pa = 0.f, pb = 0.f;
     auto fetch = [&](int base) {     // tokens base .. base + kGroup - 1 into registers
 #pragma unroll
@@ -143,15 +176,15 @@ gdr_recurrent_kernel(GdrArgs a)
         __syncthreads();             // the previous group is no longer read
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
-            const int e = tid + u * kThreads, t = e / (DK / 8), c = (e % (DK / 8)) * 8;
+            const int e = tid + u * kThreads, t = e / (DK / 8), c = (e % (DK / 8)) * 8;   // channels c .. c + 7
             float dot = 0.f;
             if (e < kPieces) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {   // channel c + i: row group (c + i) % 4
-                    const int at = ((c + i) & 3) * kLd + ((c + i) >> 2);
-                    sK[t][at] = pk[u][i];
-                    sQ[t][at] = pq[u][i];
-                    dot = fmaf(pk[u][i], pq[u][i], dot);
+                for (int i = 0; i < 8; i += 2) {   // channels c + i, + 1: row group (c + i) / 2 % 4
+                    const int at = ((i >> 1) & 3) * kLd + (c >> 2);
+                    *(float2 *)&sK[t][at] = make_float2(pk[u][i], pk[u][i + 1]);
+                    *(float2 *)&sQ[t][at] = make_float2(pq[u][i], pq[u][i + 1]);
+                    dot = fmaf(pk[u][i], pq[u][i], fmaf(pk[u][i + 1], pq[u][i + 1], dot));
                 }
             }
             // The DK / 8 lanes of one token are neighbours of one warp.
@@ -171,48 +204,53 @@ gdr_recurrent_kernel(GdrArgs a)
         __syncthreads();
         if (base + kGroup < len) fetch(base + kGroup);
         for (int t = 0; t < m; ++t) {
-            const float al = sA[t];
-            const float2 al2 = make_float2(al, al);
-            float2 seen[2] = {{0.f, 0.f}, {0.f, 0.f}}, read[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            run *= sA[t];
+            if (!(run >= 0x1p-32f && run <= 0x1p32f)) fold();
+            const float inv = __frcp_rn(run);
+            float2 n0[2] = {}, n1[2] = {}, r0[2] = {}, r1[2] = {};
 #pragma unroll
-            for (int i = 0; i < R; i += 4) {
-                const float4 k4 = *(const float4 *)&sK[t][rq * kLd + i];
-                const float4 q4 = *(const float4 *)&sQ[t][rq * kLd + i];
-                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i + j] = __fmul2_rn(s[i + j], al2);
-                    seen[j & 1] = __ffma2_rn(make_float2(kk[j], kk[j]), s[i + j], seen[j & 1]);
-                    read[j & 1] = __ffma2_rn(make_float2(qq[j], qq[j]), s[i + j], read[j & 1]);
-                }
+            for (int i = 0; i < R; i += 2) {
+                const float4 k4 = *(const float4 *)&sK[t][rq * kLd + 2 * i];
+                const float4 q4 = *(const float4 *)&sQ[t][rq * kLd + 2 * i];
+                const float2 ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
+                const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w);
+                n0[0] = __ffma2_rn(ka, s0[i], n0[0]);
+                n1[0] = __ffma2_rn(ka, s1[i], n1[0]);
+                r0[0] = __ffma2_rn(qa, s0[i], r0[0]);
+                r1[0] = __ffma2_rn(qa, s1[i], r1[0]);
+                n0[1] = __ffma2_rn(kb, s0[i + 1], n0[1]);
+                n1[1] = __ffma2_rn(kb, s1[i + 1], n1[1]);
+                r0[1] = __ffma2_rn(qb, s0[i + 1], r0[1]);
+                r1[1] = __ffma2_rn(qb, s1[i + 1], r1[1]);
             }
-            float2 sn = __fadd2_rn(seen[0], seen[1]), rd = __fadd2_rn(read[0], read[1]);
-            sn = shfl_add(sn, 8);
-            rd = shfl_add(rd, 8);
-            sn = shfl_add(sn, 16);
-            rd = shfl_add(rd, 16);
+            auto total = [&](const float2 (&x)[2]) {
+                const float2 y = __fadd2_rn(x[0], x[1]);
+                return run * group_sum(y.x + y.y);
+            };
+            const float seen0 = total(n0), seen1 = total(n1), read0 = total(r0), read1 = total(r1);
             const float2 vv = *(const float2 *)&sV[t][col - part * kCols];
             const float b = sB[t];
-            const float2 d = make_float2(b * (vv.x - sn.x), b * (vv.y - sn.y));
+            const float d0 = b * (vv.x - seen0), d1 = b * (vv.y - seen1);
             if (o && rq == 0) {
                 const float kq = sKQ[t];
                 store_pair(o + ((size_t)(t0 + base + t) * a.H + h) * DV + col,
-                           make_float2(a.scale * fmaf(kq, d.x, rd.x), a.scale * fmaf(kq, d.y, rd.y)));
+                           make_float2(a.scale * fmaf(kq, d0, read0), a.scale * fmaf(kq, d1, read1)));
             }
+            const float e0 = d0 * inv, e1 = d1 * inv;
 #pragma unroll
-            for (int i = 0; i < R; i += 4) {
-                const float4 k4 = *(const float4 *)&sK[t][rq * kLd + i];
-                const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[i + j] = __ffma2_rn(make_float2(kk[j], kk[j]), d, s[i + j]);
+            for (int i = 0; i < R; i += 2) {
+                const float4 k4 = *(const float4 *)&sK[t][rq * kLd + 2 * i];
+                const float2 ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
+                s0[i] = __ffma2_rn(ka, make_float2(e0, e0), s0[i]);
+                s1[i] = __ffma2_rn(ka, make_float2(e1, e1), s1[i]);
+                s0[i + 1] = __ffma2_rn(kb, make_float2(e0, e0), s0[i + 1]);
+                s1[i + 1] = __ffma2_rn(kb, make_float2(e1, e1), s1[i + 1]);
             }
-            if (a.block > 0) {       // a completed block: its row keeps this state
-                const int pos = ctx + base + t + 1;
-                if (pos > 0 && pos % a.block == 0 && pos / a.block <= a.table_cols) {
-                    const int row = a.table[(size_t)n * a.table_cols + pos / a.block - 1];
-                    if (row >= 0 && row < a.pool_size) write_row(row);
-                }
+            if (--to_block == 0) {       // a completed block: its row keeps this state
+                const int row = blk < a.table_cols ? a.table[(size_t)n * a.table_cols + blk] : -1;
+                if (row >= 0 && row < a.pool_size) write_row(row);
+                to_block = a.block;
+                ++blk;
             }
         }
     }
@@ -226,7 +264,10 @@ cudaError_t launch_typed(const GdrArgs &a, cudaStream_t stream)
     const int64_t blocks = (int64_t)a.num_seqs * a.H * (DV / (kThreads / 2));
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    gdr_recurrent_kernel<DK, DV, T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    if (sizeof(T) == 2 && DV >= 64 && !a.cu)
+        gdr_recurrent_kernel<DK, DV, T, sizeof(T) == 2 && DV >= 64 ? 4 : 1><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    else
+        gdr_recurrent_kernel<DK, DV, T, 1><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -87,7 +87,7 @@ def test_decode_refusals(kw, code):
     dict(cu=None), dict(head=None), dict(head_out=None), dict(new=None), dict(table=None),
     dict(free=None), dict(slots=P + 4), dict(pos=P + 2), dict(new=P + 1), dict(cu=P + 2),
     dict(table=P + 2), dict(src=P + 3), dict(dst=P + 1), dict(free=P + 2), dict(head=P + 2),
-    dict(head_out=P + 2), dict(ctx=P + 2)], ids=str)
+    dict(head_out=P + 2), dict(ctx=P + 2), dict(N=1 << 16, cols=1 << 15)], ids=str)
 def test_plan_refusals(kw):
     assert plan(**kw) == INVALID
 
