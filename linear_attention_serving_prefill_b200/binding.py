@@ -447,7 +447,7 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream,
           _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, (T, H, dv)),
           _ptr(g, "g", torch.float32, dev, (T, H)), _ptr(beta, "beta", torch.float32, dev, (T, H)),
-          _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev), host, N, T, Hk, H, dk, dv,
+          _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev, (N + 1,)), host, N, T, Hk, H, dk, dv,
           KDA_DTYPE[dt], scale, pool, rows, _ptr(src_slots, "src_slots", torch.int32, dev, (N,)),
           _ptr(dst_slots, "dst_slots", torch.int32, dev, (N,)),
           _ptr(ctx_lens, "ctx_lens", torch.int32, dev, (N,)),

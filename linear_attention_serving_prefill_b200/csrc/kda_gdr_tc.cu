@@ -13,17 +13,18 @@
 //   o_r = scale e^{G_r} (Q S + P F)_r,  S <- e^{G_C} (S + K^T F),
 // so one factor per token remains in R, one at the outputs and one at the state, and K and Q
 // enter the products as their TMA tiles.  e^{-G} has to stay in the floating-point range: a
-// chunk ends early, before the token at which |G| would pass 2^kRange; below 2^kSafe nothing
-// is shifted, between them the chunk's scale is shifted down so that e^{-G} <= 2^kSafe (state
+// chunk ends early, before the token at which e^{-G} would pass 2^200; up to 2^100 nothing is
+// shifted, between them the chunk's scale is shifted down so that e^{-G} <= 2^100 (state
 // entries below 2^-26 are then lost in that chunk, which multiplies the state by less than
 // 2^-100 anyway).  Relative accuracy is that of the decayed form: each term is scaled by a
 // power it keeps to its use.
 //
 // Precision.  K and Q are exact operands.  The others on the state's path, S, R, T and F, are
 // each the sum of two bf16 numbers (17 bits), and a product of two such sums leaves out only
-// low x low: the state comes out within about 1e-5 of the recurrence in 64 bits (2-norm),
-// where single bf16 operands gave 2.5e-3.  The outputs' own products take the high parts
-// alone, which their rounding to bf16 hides.
+// low x low: the state comes out within 4e-6 of the recurrence in 64 bits (2-norm), where
+// single bf16 operands gave 2.5e-3.  Of the outputs' own products P and S take their high part
+// alone: outputs within 2.4e-3, of which their rounding to bf16 is 1.7e-3 (S's low part too:
+// 2.2e-3, and 3.25 instead of 3.15 us a chunk).
 //
 // One CTA of 32 warps owns a (sequence, value head) and walks its chunks with the fp32 state
 // transposed in tensor memory.  Nothing goes through HBM but q, k, v, g, beta, o and the
@@ -354,12 +355,6 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(&bars.o_free, kAuxThreads);
         fence_mbar_init();
     }
-    // The upper right quadrants of P and T are zero in every chunk.
-    for (int e = tid; e < (kPBufs + 2) * 128; e += kThreads) {
-        const uint32_t img = kOffP + (e >> 7) * 8192;   // P's buffers, then T's parts
-        *(uint4 *)(sm + img + sw128_offset((e >> 2) & 31, 32 + 8 * (e & 3), 64)) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
     if (warp == 0) { tmem_alloc(&tbase, 512); tmem_relinquish(); }
     tc_fence_before_sync();
     __syncthreads();
@@ -475,7 +470,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             hand_over(&bars.f_ready);
             const int row = in.row;
             if (!last) ok = wait_info(c + 1);
-            const float f = last ? 0.f : out * infos[(c + 1) % kInfos].in;
+            // (One after the other: their product may leave the exponent range.)
+            const float next = infos[(c + 1) % kInfos].in;
             ok = ok && wait(&bars.s_full, c);
             if (!ok) break;
             tc_fence_after_sync();
@@ -498,7 +494,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                    const float2 t = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(f, f));
+                    const float2 t = __fmul2_rn(__fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(out, out)),
+                                                make_float2(next, next));
                     x[i] = t.x;
                     x[i + 1] = t.y;
                 }
@@ -736,9 +733,12 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_after_sync();
             if (leader) {   // [DF] = R^T T^T: high x low, low x high, high x high
 #pragma unroll
-                for (int ks = 0; ks < 12; ++ks)
-                    mma_ts(tdf, rf + 8 * (ks & 3) + (ks >= 4 && ks < 8 ? 32 : 0),
-                           dT + (((ks < 4 ? 8192 : 0) + (ks & 3) * 32) >> 4), id64, ks > 0);
+                for (int ks = 0; ks < 12; ++ks) {
+                    const int s16 = ks & 3;
+                    mma_ts(tdf + 16 * s16, rf + 8 * s16 + (ks >= 4 && ks < 8 ? 32 : 0),
+                           dT + (((ks < 4 ? 8192 : 0) + s16 * (2048 + 32)) >> 4),
+                           idesc_bf16_f32(128, 64 - 16 * s16), ks > 0);
+                }
                 mma_commit(&bars.f_full);
                 mma_commit(&bars.t_free[s]);
             }
@@ -761,7 +761,9 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mma_commit(&bars.s_full);
                 mma_commit(&bars.kq_empty[s]);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ts(to, rf + 8 * ks, dP + ks * (32 >> 4), id64, true);
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ts(to + 16 * (ks & 3), rf + 8 * ks, dP + (ks & 3) * ((2048 + 32) >> 4),
+                           idesc_bf16_f32(128, 64 - 16 * (ks & 3)), true);
                 mma_commit(&bars.o_full[stage]);
             }
             __syncwarp();
