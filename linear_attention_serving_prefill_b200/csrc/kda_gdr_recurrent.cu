@@ -13,23 +13,32 @@
 // 2 c + 1 (64 registers at dk = 128), both reductions of a token are two xor
 // shuffles over the four row groups, and no token step crosses warps.  Packed fp32
 // pairs run along the rows, so that the pairs of k and q come as they lie in
-// shared memory.  The decays are not applied token by token: the registers hold
+// shared memory; they are kept as 64-bit registers (as float2 the same code needed
+// 540 instead of 320 instructions a token: 148 and 122 us for the verify pass
+// below).  The decays are not applied token by token: the registers hold
 // S / run with one running factor run = prod e^{g}, folded in before it leaves
 // [2^-32, 2^32], so a token costs three packed products per row pair and column.
-// q, k, v, g and beta of kGroup tokens at a time are staged in shared memory as
-// fp32; the next group's global loads are in flight while the current one runs.
 //
-// A long sequence is bound by the latency of one token's chain (0.35 us at dk = 128,
-// 0.30 us at dk = 64: two reductions, their shuffles and the update, one after the other);
-// a verify pass of a few tokens by reading the states (64 x 96 states, 4 tokens: 139 us,
-// 3.1 TB/s).
+// Two kernels: packed sequences stage 8 tokens at a time, the next 8 on their way in
+// registers; a few tokens of each of many sequences (verify, replay) overlap one
+// state's steps with the next state's load.
+//
+// A long sequence is bound by the latency of one token's chain (two reductions, their
+// shuffles and the update, one after the other): 0.31 us a token at dk = dv = 128, 0.25 us
+// at 64.  A verify pass (64 x 96 states of 128 x 128, 4 tokens, 403 MB) takes 122 us and a
+// replay (100 x 32 key heads, 96 heads, up to 6 tokens) 246 us, 3.3 and 5.2 TB/s: the steps'
+// shared-memory loads and shuffles, at the 16 warps per SM that the states leave room for.
+// Slower, both measured: four tokens at a time from one pass over the state and a small
+// triangular solve (verify 119, replay 271 us, packed 0.38 us a token), and that with four
+// columns and half the rows per lane (115, 266 us, 0.42 us).
 #include "kda_common.cuh"
 #include "kda_gdr.h"
 
 namespace kda {
 namespace {
 
-constexpr int kGroup = 8;           // tokens staged together
+constexpr int kGroup = 8, kFew = 4;  // tokens staged together: packed sequences, a few tokens each
+constexpr int kSms = 148;
 
 // The log-decay is clamped where e^{g} is 0 in fp32 anyway; NaN passes through.
 __device__ __forceinline__ float clamp_log_decay(float g) { return g < kGClampSoftplus ? kGClampSoftplus : g; }
@@ -56,25 +65,139 @@ __device__ __forceinline__ float group_sum(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
+// Two adjacent elements as fp32.
+__device__ __forceinline__ float2 load_pair(const float *p) { return *(const float2 *)p; }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p) {
+    const uint32_t u = *(const uint32_t *)p;
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+template <int BYTES> __device__ __forceinline__ void copy_async(void *to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                 ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "n"(BYTES) : "memory");
+}
+
 // Two fp32 outputs to adjacent storage elements.
 __device__ __forceinline__ void store_pair(float *p, float2 x) { *(float2 *)p = x; }
 __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 x) {
     *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x.x, x.y);
 }
 
-// kMinBlocks: 4 (128 registers, a few of them spilled at dk = 128) holds more states per SM
-// and wins where each sequence has a few tokens and loading the states counts; 1 wins over
-// long sequences.  bf16, dk = dv = 128, 4 / 1: verify of 64 x 4 tokens, 32 heads 139 / 146 us;
-// replay of 256 x up to 8 tokens 265 / 285 us.  dv = 64, prefill of 2048 tokens, 16 heads:
-// 1112 / 836 us.
-template <int DK, int DV, typename T, int kMinBlocks>
-__global__ void __launch_bounds__(DV >= 64 ? 128 : 64, kMinBlocks)
+// Packed fp32 pairs as 64-bit registers.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 both(Pair p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The columns col, col + 1 of one state for a lane: row pairs 8 i + 2 rq, + 1, over run.
+template <int DK, int DV> struct Columns {
+    static constexpr int R = DK / 8, kLd = DK / 4 + 4;   // row pairs; stride of a row group in a staged vector
+    Pair s0[R], s1[R];
+    float run;
+
+    __device__ __forceinline__ void set(int i, float2 x, float2 y) {   // rows of pair i
+        s0[i] = pair(x.x, y.x);
+        s1[i] = pair(x.y, y.y);
+    }
+    // p: row 2 rq, column col of a state.
+    __device__ __forceinline__ void load(const float *p) {
+        run = 1.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (p)
+                set(i, *(const float2 *)(p + (size_t)8 * i * DV), *(const float2 *)(p + (size_t)(8 * i + 1) * DV));
+            else
+                s0[i] = s1[i] = 0;
+        }
+    }
+    __device__ __forceinline__ void store(float *p) const {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float2 x = both(s0[i]), y = both(s1[i]);
+            *(float2 *)(p + (size_t)8 * i * DV) = make_float2(run * x.x, run * y.x);
+            *(float2 *)(p + (size_t)(8 * i + 1) * DV) = make_float2(run * x.y, run * y.y);
+        }
+    }
+    // One token: k and q this lane's row group of the staged vectors, kq their product, b beta;
+    // returns the outputs before their scale.
+    __device__ __forceinline__ float2 token(const float *k, const float *q, float decay, float b, float kq, float2 v) {
+        run *= decay;
+        if (!(run >= 0x1p-32f && run <= 0x1p32f)) {      // into the state
+            const Pair f = pair(run, run);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                s0[i] = mul2(s0[i], f);
+                s1[i] = mul2(s1[i], f);
+            }
+            run = 1.f;
+        }
+        Pair n0[2] = {}, n1[2] = {}, r0[2] = {}, r1[2] = {};
+#pragma unroll
+        for (int i = 0; i < R; i += 2) {
+            const ulonglong2 kk = *(const ulonglong2 *)(k + 2 * i), qq = *(const ulonglong2 *)(q + 2 * i);
+            n0[0] = fma2(kk.x, s0[i], n0[0]);
+            n1[0] = fma2(kk.x, s1[i], n1[0]);
+            r0[0] = fma2(qq.x, s0[i], r0[0]);
+            r1[0] = fma2(qq.x, s1[i], r1[0]);
+            n0[1] = fma2(kk.y, s0[i + 1], n0[1]);
+            n1[1] = fma2(kk.y, s1[i + 1], n1[1]);
+            r0[1] = fma2(qq.y, s0[i + 1], r0[1]);
+            r1[1] = fma2(qq.y, s1[i + 1], r1[1]);
+        }
+        auto total = [&](const Pair (&x)[2]) {
+            const float2 y = both(x[0]), z = both(x[1]);
+            return run * group_sum((y.x + z.x) + (y.y + z.y));
+        };
+        const float seen0 = total(n0), seen1 = total(n1), read0 = total(r0), read1 = total(r1);
+        const float d0 = b * (v.x - seen0), d1 = b * (v.y - seen1);
+        const float inv = __frcp_rn(run);
+        const Pair e0 = pair(d0 * inv, d0 * inv), e1 = pair(d1 * inv, d1 * inv);
+#pragma unroll
+        for (int i = 0; i < R; i += 2) {
+            const ulonglong2 kk = *(const ulonglong2 *)(k + 2 * i);
+            s0[i] = fma2(kk.x, e0, s0[i]);
+            s1[i] = fma2(kk.x, e1, s1[i]);
+            s0[i + 1] = fma2(kk.y, e0, s0[i + 1]);
+            s1[i + 1] = fma2(kk.y, e1, s1[i + 1]);
+        }
+        return make_float2(fmaf(kq, d0, read0), fmaf(kq, d1, read1));
+    }
+};
+
+// Channels c .. c + 7 of a vector into its staged form: four row groups, channels 8 i + 2 rq, + 1
+// of group rq in a row of kLd.
+template <int kLd> __device__ __forceinline__ void stage8(float *to, int c, const float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) *(float2 *)&to[(i >> 1) * kLd + (c >> 2)] = make_float2(x[i], x[i + 1]);
+}
+
+template <int DV> constexpr int kWarpsOf = DV >= 64 ? 4 : 2;
+
+// Packed sequences.
+template <int DK, int DV, typename T>
+__global__ void __launch_bounds__(32 * kWarpsOf<DV>, 1)
 gdr_recurrent_kernel(GdrArgs a)
 {
-    constexpr int kWarps = DV >= 64 ? 4 : 2, kThreads = 32 * kWarps;
+    using Cols = Columns<DK, DV>;
+    constexpr int kWarps = kWarpsOf<DV>, kThreads = 32 * kWarps, kLd = Cols::kLd;
     constexpr int kCols = 16 * kWarps;           // value columns of this CTA
-    constexpr int R = DK / 8;                    // row pairs per lane
-    constexpr int kLd = DK / 4 + 4;              // row-group stride: distinct banks for the four groups
     constexpr int kPieces = kGroup * DK / 8;     // 8-element pieces of one staged operand
     constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
     constexpr int kVPieces = kGroup * kCols / 8;
@@ -91,56 +214,18 @@ gdr_recurrent_kernel(GdrArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rq = lane >> 3, col = part * kCols + 16 * warp + 2 * (lane & 7);
 
-    int64_t t0;
-    int len;
-    if (a.cu) {
-        const int lo = max(a.cu[n], 0), hi = min(a.cu[n + 1], a.total_tokens);
-        t0 = lo;
-        len = max(hi - lo, 0);
-    } else {
-        t0 = (int64_t)n * a.Tq;
-        len = a.num_tokens ? min(max(a.num_tokens[n], 0), a.Tq) : a.Tq;
-    }
+    const int64_t t0 = max(a.cu[n], 0);
+    const int len = max(min(a.cu[n + 1], a.total_tokens) - (int)t0, 0);
     // Pool rows: outside [0, pool_size) the state starts from zero / is not written.
-    int src = a.src ? a.src[n] : (a.cu ? -1 : n);
-    int dst = a.dst ? a.dst[n] : (a.cu ? -1 : src);
+    int src = a.src ? a.src[n] : -1, dst = a.dst ? a.dst[n] : -1;
     if (!a.state || src < 0 || src >= a.pool_size) src = -1;
-    if (!a.state || !a.update || dst < 0 || dst >= a.pool_size) dst = -1;
+    if (!a.state || dst < 0 || dst >= a.pool_size) dst = -1;
     if (len == 0 && dst < 0) return;
     const size_t own = (size_t)(2 * rq) * DV + col;    // row 2 rq, this lane's column pair
     auto row_of = [&](int slot) { return a.state + ((size_t)slot * a.H + h) * DK * DV + own; };
 
-    float2 s0[R], s1[R];     // row pairs of columns col and col + 1, over run
-    float run = 1.f;
-    {
-        const float *p = src >= 0 ? row_of(src) : nullptr;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float2 x = make_float2(0.f, 0.f), y = x;
-            if (p) {
-                x = *(const float2 *)(p + (size_t)8 * i * DV);
-                y = *(const float2 *)(p + (size_t)(8 * i + 1) * DV);
-            }
-            s0[i] = make_float2(x.x, y.x);
-            s1[i] = make_float2(x.y, y.y);
-        }
-    }
-    auto fold = [&] {        // run into the state
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            s0[i] = __fmul2_rn(s0[i], make_float2(run, run));
-            s1[i] = __fmul2_rn(s1[i], make_float2(run, run));
-        }
-        run = 1.f;
-    };
-    auto write_row = [&](int slot) {
-        float *p = row_of(slot);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            *(float2 *)(p + (size_t)8 * i * DV) = make_float2(run * s0[i].x, run * s1[i].x);
-            *(float2 *)(p + (size_t)(8 * i + 1) * DV) = make_float2(run * s0[i].y, run * s1[i].y);
-        }
-    };
+    Cols S;
+    S.load(src >= 0 ? row_of(src) : nullptr);
 
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v;
     T *o = (T *)a.o;
@@ -179,13 +264,10 @@ gdr_recurrent_kernel(GdrArgs a)
             const int e = tid + u * kThreads, t = e / (DK / 8), c = (e % (DK / 8)) * 8;   // channels c .. c + 7
             float dot = 0.f;
             if (e < kPieces) {
+                stage8<kLd>(sK[t], c, pk[u]);
+                stage8<kLd>(sQ[t], c, pq[u]);
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {   // channels c + i, + 1: row group (c + i) / 2 % 4
-                    const int at = ((i >> 1) & 3) * kLd + (c >> 2);
-                    *(float2 *)&sK[t][at] = make_float2(pk[u][i], pk[u][i + 1]);
-                    *(float2 *)&sQ[t][at] = make_float2(pq[u][i], pq[u][i + 1]);
-                    dot = fmaf(pk[u][i], pq[u][i], fmaf(pk[u][i + 1], pq[u][i + 1], dot));
-                }
+                for (int i = 0; i < 8; ++i) dot = fmaf(pk[u][i], pq[u][i], dot);
             }
             // The DK / 8 lanes of one token are neighbours of one warp.
 #pragma unroll
@@ -204,70 +286,165 @@ gdr_recurrent_kernel(GdrArgs a)
         __syncthreads();
         if (base + kGroup < len) fetch(base + kGroup);
         for (int t = 0; t < m; ++t) {
-            run *= sA[t];
-            if (!(run >= 0x1p-32f && run <= 0x1p32f)) fold();
-            const float inv = __frcp_rn(run);
-            float2 n0[2] = {}, n1[2] = {}, r0[2] = {}, r1[2] = {};
-#pragma unroll
-            for (int i = 0; i < R; i += 2) {
-                const float4 k4 = *(const float4 *)&sK[t][rq * kLd + 2 * i];
-                const float4 q4 = *(const float4 *)&sQ[t][rq * kLd + 2 * i];
-                const float2 ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
-                const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w);
-                n0[0] = __ffma2_rn(ka, s0[i], n0[0]);
-                n1[0] = __ffma2_rn(ka, s1[i], n1[0]);
-                r0[0] = __ffma2_rn(qa, s0[i], r0[0]);
-                r1[0] = __ffma2_rn(qa, s1[i], r1[0]);
-                n0[1] = __ffma2_rn(kb, s0[i + 1], n0[1]);
-                n1[1] = __ffma2_rn(kb, s1[i + 1], n1[1]);
-                r0[1] = __ffma2_rn(qb, s0[i + 1], r0[1]);
-                r1[1] = __ffma2_rn(qb, s1[i + 1], r1[1]);
-            }
-            auto total = [&](const float2 (&x)[2]) {
-                const float2 y = __fadd2_rn(x[0], x[1]);
-                return run * group_sum(y.x + y.y);
-            };
-            const float seen0 = total(n0), seen1 = total(n1), read0 = total(r0), read1 = total(r1);
-            const float2 vv = *(const float2 *)&sV[t][col - part * kCols];
-            const float b = sB[t];
-            const float d0 = b * (vv.x - seen0), d1 = b * (vv.y - seen1);
-            if (o && rq == 0) {
-                const float kq = sKQ[t];
-                store_pair(o + ((size_t)(t0 + base + t) * a.H + h) * DV + col,
-                           make_float2(a.scale * fmaf(kq, d0, read0), a.scale * fmaf(kq, d1, read1)));
-            }
-            const float e0 = d0 * inv, e1 = d1 * inv;
-#pragma unroll
-            for (int i = 0; i < R; i += 2) {
-                const float4 k4 = *(const float4 *)&sK[t][rq * kLd + 2 * i];
-                const float2 ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
-                s0[i] = __ffma2_rn(ka, make_float2(e0, e0), s0[i]);
-                s1[i] = __ffma2_rn(ka, make_float2(e1, e1), s1[i]);
-                s0[i + 1] = __ffma2_rn(kb, make_float2(e0, e0), s0[i + 1]);
-                s1[i + 1] = __ffma2_rn(kb, make_float2(e1, e1), s1[i + 1]);
-            }
+            const float2 y = S.token(&sK[t][rq * kLd], &sQ[t][rq * kLd], sA[t], sB[t], sKQ[t],
+                                     *(const float2 *)&sV[t][col - part * kCols]);
+            if (rq == 0)
+                store_pair(o + ((size_t)(t0 + base + t) * a.H + h) * DV + col, make_float2(a.scale * y.x, a.scale * y.y));
             if (--to_block == 0) {       // a completed block: its row keeps this state
                 const int row = blk < a.table_cols ? a.table[(size_t)n * a.table_cols + blk] : -1;
-                if (row >= 0 && row < a.pool_size) write_row(row);
+                if (row >= 0 && row < a.pool_size) S.store(row_of(row));
                 to_block = a.block;
                 ++blk;
             }
         }
     }
-    if (dst >= 0 && (len > 0 || dst != src)) write_row(dst);
+    if (dst >= 0 && (len > 0 || dst != src)) S.store(row_of(dst));
+}
+
+// A few tokens of each of many sequences.  A CTA walks over states; while it applies one
+// state's tokens, the next state's columns and tokens are on their way into shared memory
+// (cp.async; a thread fetches what it keeps, so the state needs no barrier), so that loads
+// and steps overlap although a state fills the registers.
+template <int DK, int DV, typename T>
+__global__ void __launch_bounds__(32 * kWarpsOf<DV>, 16 / kWarpsOf<DV>)
+gdr_few_kernel(GdrArgs a, int64_t items)
+{
+    using Cols = Columns<DK, DV>;
+    constexpr int kWarps = kWarpsOf<DV>, kThreads = 32 * kWarps, kLd = Cols::kLd, R = Cols::R;
+    constexpr int kCols = 16 * kWarps, kParts = DV / kCols;
+    constexpr int kPieces = kFew * DK / 8;
+    constexpr int kEl = 16 / sizeof(T);          // elements of a 16-byte copy
+    __shared__ __align__(16) float2 sS[2 * R][kThreads];
+    __shared__ __align__(16) T rK[kFew][DK], rQ[kFew][DK], rV[2][kFew][kCols];
+    __shared__ __align__(16) float sK[kFew][4 * kLd], sQ[kFew][4 * kLd];
+    __shared__ float rG[kFew], rB[kFew], sA[kFew], sB[kFew], sKQ[kFew];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rq = lane >> 3, own_col = 16 * warp + 2 * (lane & 7);
+    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v;
+    T *o = (T *)a.o;
+
+    struct Item { int n, h, part, src, dst, len; };
+    auto item_at = [&](int64_t it) {
+        Item x;
+        x.part = (int)(it % kParts);
+        const int64_t chain = it / kParts;
+        x.n = (int)(chain / a.H);
+        x.h = (int)(chain - (int64_t)x.n * a.H);
+        x.len = a.num_tokens ? min(max(a.num_tokens[x.n], 0), a.Tq) : a.Tq;
+        // Pool rows: outside [0, pool_size) the state starts from zero / is not written.
+        x.src = a.src ? a.src[x.n] : x.n;
+        x.dst = a.dst ? a.dst[x.n] : x.src;
+        if (x.src < 0 || x.src >= a.pool_size) x.src = -1;
+        if (!a.update || x.dst < 0 || x.dst >= a.pool_size || (x.len == 0 && x.dst == x.src)) x.dst = -1;
+        return x;
+    };
+    auto state_at = [&](const Item &x, int slot) {   // row 2 rq, this lane's column pair
+        return a.state + ((size_t)slot * a.H + x.h) * DK * DV + (size_t)(2 * rq) * DV + x.part * kCols + own_col;
+    };
+    int buf = 0;                   // rV's half that the next copies go to
+    auto fetch_tokens = [&](const Item &x, int base) {
+        const int hk = x.h / (a.H / a.Hk), m = min(kFew, x.len - base);
+        const size_t t0 = (size_t)x.n * a.Tq + base;
+        for (int e = tid; e < m * (DK / kEl); e += kThreads) {
+            const int t = e / (DK / kEl), c = (e % (DK / kEl)) * kEl;
+            const size_t at = ((t0 + t) * a.Hk + hk) * DK + c;
+            copy_async<16>(&rK[t][c], k + at);
+            copy_async<16>(&rQ[t][c], q + at);
+        }
+        for (int e = tid; e < m * (kCols / kEl); e += kThreads) {
+            const int t = e / (kCols / kEl), c = (e % (kCols / kEl)) * kEl;
+            copy_async<16>(&rV[buf][t][c], v + ((t0 + t) * a.H + x.h) * DV + x.part * kCols + c);
+        }
+        if (tid < m) {
+            copy_async<4>(&rG[tid], a.g + (t0 + tid) * a.H + x.h);
+            copy_async<4>(&rB[tid], a.beta + (t0 + tid) * a.H + x.h);
+        }
+    };
+    auto fetch = [&](const Item &x) {
+        if (x.len == 0 && x.dst < 0) return;
+        if (x.src >= 0) {
+            const float *p = state_at(x, x.src);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                copy_async<8>(&sS[2 * i][tid], p + (size_t)8 * i * DV);
+                copy_async<8>(&sS[2 * i + 1][tid], p + (size_t)(8 * i + 1) * DV);
+            }
+        }
+        fetch_tokens(x, 0);
+    };
+
+    int64_t it = blockIdx.x;
+    Item x = item_at(it);          // (no more CTAs than items)
+    fetch(x);
+    for (;;) {
+        const bool more = it + gridDim.x < items;
+        Item next = x;
+        if (more) next = item_at(it + gridDim.x);
+        Cols S;
+        S.run = 1.f;
+        for (int base = 0; base == 0 || base < x.len; base += kFew) {
+            const int m = min(kFew, x.len - base);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (base == 0) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float2 zero = make_float2(0.f, 0.f);
+                    S.set(i, x.src >= 0 ? sS[2 * i][tid] : zero, x.src >= 0 ? sS[2 * i + 1][tid] : zero);
+                }
+            }
+            __syncthreads();       // every thread's copies are here; the previous tokens are no longer read
+            for (int e0 = 0; e0 < kPieces; e0 += kThreads) {
+                const int e = e0 + tid, t = e / (DK / 8), c = (e % (DK / 8)) * 8;
+                float dot = 0.f;
+                if (e < kPieces && t < m) {
+                    float xk[8], xq[8];
+                    load8(&rK[t][c], xk);
+                    load8(&rQ[t][c], xq);
+                    stage8<kLd>(sK[t], c, xk);
+                    stage8<kLd>(sQ[t], c, xq);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot = fmaf(xk[i], xq[i], dot);
+                }
+#pragma unroll
+                for (int off = 1; off < DK / 8; off <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                if (e < kPieces && t < m && e % (DK / 8) == 0) sKQ[t] = dot;
+            }
+            if (tid < m) { sA[tid] = expf(clamp_log_decay(rG[tid])); sB[tid] = rB[tid]; }
+            buf ^= 1;
+            __syncthreads();       // staged; the buffers of the copies are free
+            if (base + kFew < x.len) fetch_tokens(x, base + kFew);
+            else if (more) fetch(next);
+            const size_t t0 = (size_t)x.n * a.Tq + base;
+#pragma unroll 1
+            for (int t = 0; t < m; ++t) {
+                const float2 y = S.token(&sK[t][rq * kLd], &sQ[t][rq * kLd], sA[t], sB[t], sKQ[t],
+                                         load_pair(&rV[buf ^ 1][t][own_col]));
+                if (o && rq == 0)
+                    store_pair(o + ((t0 + t) * a.H + x.h) * DV + x.part * kCols + own_col,
+                               make_float2(a.scale * y.x, a.scale * y.y));
+            }
+        }
+        if (x.dst >= 0) S.store(state_at(x, x.dst));
+        if (!more) break;
+        it += gridDim.x;
+        x = next;
+    }
 }
 
 template <int DK, int DV, typename T>
 cudaError_t launch_typed(const GdrArgs &a, cudaStream_t stream)
 {
-    constexpr int kThreads = DV >= 64 ? 128 : 64;
-    const int64_t blocks = (int64_t)a.num_seqs * a.H * (DV / (kThreads / 2));
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (sizeof(T) == 2 && DV >= 64 && !a.cu)
-        gdr_recurrent_kernel<DK, DV, T, sizeof(T) == 2 && DV >= 64 ? 4 : 1><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
-    else
-        gdr_recurrent_kernel<DK, DV, T, 1><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    constexpr int kThreads = 32 * kWarpsOf<DV>;
+    const int64_t items = (int64_t)a.num_seqs * a.H * (DV / (kThreads / 2));
+    if (items == 0) return cudaSuccess;
+    if (a.cu) {
+        if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+        gdr_recurrent_kernel<DK, DV, T><<<(unsigned)items, kThreads, 0, stream>>>(a);
+    } else {
+        const int64_t resident = (int64_t)kSms * (16 / kWarpsOf<DV>);
+        gdr_few_kernel<DK, DV, T><<<(unsigned)(items < resident ? items : resident), kThreads, 0, stream>>>(a, items);
+    }
     return cudaGetLastError();
 }
 
