@@ -431,7 +431,9 @@ size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, in
  *                   device offsets may end before total_tokens (a padded batch):
  *                   rows of o behind the last sequence are left as they were.
  *                   cu_seqlens_host, when given, must end at total_tokens; it
- *                   only sets the order in which sequences start.
+ *                   only sets the order in which sequences start and how the long ones
+ *                   of a batch with few (sequence, head) pairs are divided over the
+ *                   device (without it they are taken as equally long).
  *   state, pool_size  the pool, or NULL with 0 (zero initial states, no final
  *                   state; then src_slots, dst_slots and block_size must be
  *                   absent too).
@@ -450,7 +452,7 @@ size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, in
  *                   block's row; columns past block_table_cols have no row.
  *                   block_size = 0: no such rows (block_table may be NULL).
  *   workspace       at least kda_gdr_prefill_workspace_size bytes, 16-byte aligned
- *                   (NULL when that is 0).
+ *                   (NULL when that is 0); not shared by calls that may run at once.
  *   algo            KDA_ALGO_AUTO (tensor cores for bf16 with dk = dv = 128, else the
  *                   fp32 recurrence on CUDA cores), KDA_ALGO_CUDA_CORE or
  *                   KDA_ALGO_TENSOR_CORE (KDA_ERR_UNSUPPORTED for other types or

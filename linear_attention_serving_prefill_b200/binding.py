@@ -432,6 +432,8 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     need = _lib.kda_gdr_prefill_workspace_size(T, N, Hk, H, dk, dv, KDA_DTYPE[dt], KDA_ALGO[algo])
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
     host = None
     if cu_seqlens_host is not None:
         if cu_seqlens_host.numel() != N + 1:

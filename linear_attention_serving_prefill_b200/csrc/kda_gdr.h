@@ -23,7 +23,7 @@ struct GdrArgs {
     void *o;                        // [tokens, H, dv] (decode: nullptr = no outputs)
     // Prefill: packed sequences, snapshots.
     const int32_t *cu;              // device [num_seqs + 1]; nullptr = decode layout
-    const int32_t *cu_host;         // host copy or nullptr (launch order only)
+    const int32_t *cu_host;         // host copy or nullptr (launch order, segments)
     const int32_t *ctx;             // tokens before this call, or nullptr = 0
     const int32_t *table;           // [num_seqs, table_cols] or nullptr
     int32_t table_cols, block;      // block = 0: no snapshots
@@ -41,8 +41,10 @@ cudaError_t launch_gdr_recurrent(const GdrArgs &a, cudaStream_t stream);
 // One token per sequence (a.Tq == 1), one pass over each state.
 cudaError_t launch_gdr_step(const GdrArgs &a, cudaStream_t stream);
 
-// Chunked prefill on tensor cores (bf16, dk = dv = 128; a.cu and a.status set).
-cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream);
+// Chunked prefill on tensor cores (bf16, dk = dv = 128; a.cu and a.status set), with a workspace
+// of gdr_tensor_core_workspace bytes, 16-byte aligned.
+size_t gdr_tensor_core_workspace(int32_t total_tokens, int32_t num_seqs, int32_t H);
+cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream_t stream);
 
 struct BlockPlanArgs {
     const int32_t *new_lens, *ctx_lens;

@@ -50,8 +50,8 @@ extern "C" size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t n
                                                  int32_t H, int32_t dk, int32_t dv, kda_dtype dt,
                                                  kda_algo algo)
 {
-    (void)check_prefill(total_tokens, num_seqs, Hk, H, dk, dv, dt, algo);
-    return 0;   // every path keeps its intermediates on chip
+    if (check_prefill(total_tokens, num_seqs, Hk, H, dk, dv, dt, algo) != KDA_OK) return 0;
+    return use_tensor_core(dk, dv, dt, algo) ? kda::gdr_tensor_core_workspace(total_tokens, num_seqs, H) : 0;
 }
 
 extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *v, const float *g,
@@ -65,7 +65,6 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
                                       int32_t block_size, void *o, void *workspace,
                                       size_t workspace_bytes, kda_algo algo, void *stream)
 {
-    (void)workspace_bytes;
     const kda_status st = check_prefill(total_tokens, num_seqs, Hk, H, dk, dv, dt, algo);
     if (st != KDA_OK) return st;
     if (!isfinite(scale) || pool_size < 0 || block_size < 0 || block_size % 64 != 0 ||
@@ -87,6 +86,8 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
         for (int32_t i = 0; i < num_seqs; ++i)
             if (cu_seqlens_host[i + 1] < cu_seqlens_host[i]) return KDA_ERR_INVALID_ARG;
     }
+    const size_t need = kda_gdr_prefill_workspace_size(total_tokens, num_seqs, Hk, H, dk, dv, dt, algo);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (num_seqs == 0) return KDA_OK;
 
     kda::GdrArgs a{};
@@ -103,7 +104,7 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
     if (!use_tensor_core(dk, dv, dt, algo))
         return status_of(kda::launch_gdr_recurrent(a, (cudaStream_t)stream));
     if (!kda::device_status_word(&a.status)) return KDA_ERR_CUDA;
-    return status_of(kda::launch_gdr_tensor_core(a, (cudaStream_t)stream));
+    return status_of(kda::launch_gdr_tensor_core(a, workspace, (cudaStream_t)stream));
 }
 
 extern "C" kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const float *g,

@@ -41,6 +41,11 @@
 //   info  (warp 31)      chunk bounds and factors (a warp scan).
 // K and Q are loaded twice (the second time from L2): A and P are formed up to three chunks
 // ahead of the state, and a tile that stayed for both uses would sit idle in between.
+// One chain takes 3.1 us a chunk alone and 3.15 us at 96 CTAs (32768 tokens x 96 heads: 1.61 ms):
+// the state's way through three products and three passes of the chain warps, about 6000 cycles,
+// next to the other roles, which take as long (A and P wait for one accumulator).  Tried and
+// slower: fewer, wider chain warps; register splits between roles; deeper tile rings in place of
+// the second load; TMA stores of o; unrolled waits and loops (instruction cache).
 // Products (TMEM accumulators in brackets), chunk c:
 //   [AP] = [K; Q] K^T;  [DF] = S^T K^T;  [O^T] = S^T Q^T;  [DF] = R^T T^T;
 //   [S^T] += F^T K;  [O^T] += F^T P^T
@@ -122,11 +127,33 @@ struct __align__(16) Info {
     int pad[2];
 };
 
+// One CTA per head and item.  Few chains leave most of the device idle, so long sequences are then
+// cut into segments of whole chunks.  A segment maps its incoming state S to M S + L (columns never
+// mix), so a first launch finds, for every segment but the last, L (the chain from zeros) and M (the
+// chain from the identity, with v = 0); a short second one composes the incoming states; a third
+// runs all segments with them.  Segment 0 needs no M: its L starts from the sequence's own state.
+enum Kind : uint8_t { kOutputs, kOffset, kMap };
+struct Item {
+    uint16_t seq, buf;      // first workspace buffer of the sequence: S, L of segments 0 .., M of segments 1 ..
+    uint8_t part, parts;    // segment, of how many
+    Kind kind;
+};
+constexpr int kSms = 148;   // CTAs at once: a split fills them at most once per launch
+constexpr int kMinSplit = 16 * kC, kMaxParts = 64;   // tokens of a call; segments of a sequence
+constexpr int kSplitCost = 3;                        // of the two more launches, in chunks
+
 struct Params {
     GdrArgs a;
-    bool ordered;
-    uint16_t order[kGdrMaxOrder];   // sequence of launch position i, longest first
+    float *ws;
+    bool ordered, split;
+    union {
+        uint16_t order[kGdrMaxOrder];   // sequence of launch position i, longest first
+        Item items[kSms];               // of launch position i, in a split
+    };
 };
+
+// Segment of a sequence of len tokens, in tokens.
+__device__ __forceinline__ int segment_of(int len, int parts) { return ((len + kC - 1) / kC + parts - 1) / parts * kC; }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -308,18 +335,35 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pos = blockIdx.x / a.H, h = blockIdx.x % a.H, hk = h / (a.H / a.Hk);
-    const int n = prm.ordered ? prm.order[pos] : pos;
-    const int tbeg = max(a.cu[n], 0), len = max(min(a.cu[n + 1], a.total_tokens) - tbeg, 0);
-    const int ctx = a.ctx ? max(a.ctx[n], 0) : 0;
-    int src = a.src ? a.src[n] : -1, dst = a.dst ? a.dst[n] : -1;
-    if (!a.state || src < 0 || src >= a.pool_size) src = -1;
-    if (!a.state || dst < 0 || dst >= a.pool_size) dst = -1;
+    Item it = {0, 0, 0, 1, kOutputs};
+    if (prm.split) it = prm.items[pos];
+    const int n = prm.split ? it.seq : prm.ordered ? prm.order[pos] : pos;
+    int tbeg = max(a.cu[n], 0), len = max(min(a.cu[n + 1], a.total_tokens) - tbeg, 0);
+    // This segment; those behind the sequence's end (the host's lengths may differ) do nothing.
+    const int seg = segment_of(len, it.parts), from = min((int64_t)len, (int64_t)it.part * seg);
+    const bool final = len - from <= seg;
+    if (it.part > 0 && from == len || it.kind != kOutputs && final) return;
+    tbeg += from;
+    len = final ? len - from : seg;
+    const int64_t before = (int64_t)(a.ctx ? max(a.ctx[n], 0) : 0) + from;   // tokens before this segment
+    const int src = a.src ? a.src[n] : -1, dst = a.dst ? a.dst[n] : -1;
     auto row_of = [&](int slot) { return a.state + ((size_t)slot * a.H + h) * kD * kD; };
+    auto buffer = [&](int b) { return prm.ws + ((size_t)(it.buf + b) * a.H + h) * kD * kD; };
+    const float *Sin = nullptr;                      // nullptr: zeros, or the identity
+    float *Sout = nullptr;
+    if (it.part > 0)
+        Sin = it.kind == kOutputs ? buffer(it.part) : nullptr;
+    else if (a.state && src >= 0 && src < a.pool_size)
+        Sin = prm.split && it.parts > 1 && it.kind == kOutputs ? buffer(0) : row_of(src);
+    if (it.kind != kOutputs)
+        Sout = buffer(it.kind == kMap ? it.parts - 1 + it.part : 1 + it.part);
+    else if (final && a.state && dst >= 0 && dst < a.pool_size)
+        Sout = row_of(dst);
 
     if (len == 0) {   // the state passes through
-        if (dst >= 0 && dst != src) {
-            float4 *to = (float4 *)row_of(dst);
-            const float4 *from = src >= 0 ? (const float4 *)row_of(src) : nullptr;
+        if (Sout && Sout != Sin) {
+            float4 *to = (float4 *)Sout;
+            const float4 *from = (const float4 *)Sin;
 #pragma unroll 1
             for (int e = tid; e < kD * kD / 4; e += kThreads)
                 to[e] = from ? from[e] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -381,7 +425,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp < kIntraWarp) {
         // ------------------------------------------------------------- chain --
         const int j = tid & 127, hh = warp >> 2;   // value channel; quarter of tokens / key channels
-        const float *S0 = src >= 0 ? row_of(src) + (size_t)(32 * hh) * kD + j : nullptr;
+        const bool map = it.kind == kMap;
         // 16 columns of an accumulator as two bf16 operands of 8 columns each.
         auto put16 = [&](const float (&x)[16], uint32_t hi, uint32_t lo) {
             float h[8], l[8];
@@ -406,7 +450,10 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             float x[16];
             const float f = infos[0].in;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = S0 ? S0[(size_t)(16 * p + i) * kD] * f : 0.f;
+            for (int i = 0; i < 16; ++i) {
+                const int row = 32 * hh + 16 * p + i;
+                x[i] = Sin ? Sin[(size_t)row * kD + j] * f : map && row == j ? f : 0.f;
+            }
             tmem_st16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
             put16(x, kTSb + 16 * hh + 8 * p, kTSb + 64 + 16 * hh + 8 * p);
         }
@@ -419,8 +466,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const float out = in.out;
             // V of this thread's channel and quarter of the tokens.
             ok = wait(&bars.v_full[c & 1], c >> 1);
-            float2 w[8];      // beta e^{-G} V^T
-            {
+            float2 w[8] = {};      // beta e^{-G} V^T
+            if (!map) {
                 const uint8_t *vt = sm + kOffV + (c & 1) * kVStage + (j >> 6) * 8192 + 16 * hh * 128;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -478,11 +525,12 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (row >= 0 || last) {   // rows that keep the state after this chunk
 #pragma unroll 1
                 for (int w = 0; w < 4; ++w) {
-                    const int to = w < 2 ? row : (last ? dst : -1), p = w & 1;
-                    if (to < 0) continue;
+                    float *to = w >= 2 ? (last ? Sout : nullptr) : row >= 0 ? row_of(row) : nullptr;
+                    const int p = w & 1;
+                    if (!to) continue;
                     tmem_ld16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
                     tmem_ld_wait();
-                    float *Sf = row_of(to) + (size_t)(32 * hh + 16 * p) * kD + j;
+                    float *Sf = to + (size_t)(32 * hh + 16 * p) * kD + j;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) Sf[(size_t)i * kD] = x[i] * out;
                 }
@@ -669,6 +717,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             next_stage();
             const Info &in = infos[c % kInfos];
             const bool last = in.last != 0;
+            const int rows = it.kind == kOutputs ? in.len : 0;
             tc_fence_after_sync();
             // 16 tokens at a time: four 8 x 8 blocks (channels x tokens) become eight token rows of 32
             // channels, 16-byte pieces swizzled by token pair; a lane then stores two of them.
@@ -692,7 +741,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 for (int j = 0; j < 2; ++j) {
                     const int t = q + 8 * j + (lane >> 2);
                     const uint4 w = *(const uint4 *)(ost + j * 512 + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4));
-                    if (t < in.len)
+                    if (t < rows)
                         *(uint4 *)(o + ((size_t)(tbeg + in.start + t) * a.H + h) * kD + 32 * wq + 8 * (lane & 3)) = w;
                 }
                 __syncwarp();
@@ -865,7 +914,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // -------------------------------------------------------------- info --
         int start = 0;
         // Tokens left in the current block, and its index (no blocks: more than there are).
-        int to_block = a.block > 0 ? a.block - ctx % a.block : 0x7fffffff, blk = a.block > 0 ? ctx / a.block : 0;
+        int to_block = a.block > 0 ? a.block - (int)(before % a.block) : 0x7fffffff;
+        int64_t blk = a.block > 0 ? before / a.block : 0;
         // g and beta of tokens 2 lane, 2 lane + 1 of this chunk, and of the next if this one is full.
         float g[2], be[2], gn[2], bn[2];
         auto fetch = [&](int from, float (&g)[2], float (&be)[2]) {
@@ -926,7 +976,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 in.len = m;
                 in.last = start + m >= len;
                 in.row = -1;
-                if (a.block > 0 && m == to_block && blk < a.table_cols) {
+                if (a.block > 0 && it.kind == kOutputs && m == to_block && blk < a.table_cols) {
                     const int row = a.table[(size_t)n * a.table_cols + blk];
                     if (row >= 0 && row < a.pool_size) in.row = row;
                 }
@@ -951,9 +1001,135 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == 0) tmem_dealloc(tb, 512);
 }
 
+// Composes the segments' incoming states: S_{p+1} = M_p S_p + L_p, over L_p (S_1 is L_0), 16 value
+// columns per CTA in fp32; and keeps a copy of the sequence's own state, which a later segment's
+// row may overwrite.  3.3 us a segment; wider column blocks per warp (fewer reads of M), scalar
+// products and an earlier load of L changed that by 5 % either way.
+constexpr int kJoinCols = 16, kJoinThreads = 256, kLdM = kD + 4;
+constexpr uint32_t kJoinSmem = (2 * kD * kLdM + kD * kJoinCols) * 4;
+struct Joins {
+    GdrArgs a;
+    float *ws;
+    Item items[kSms / 2];      // the split sequences
+};
+__global__ void __launch_bounds__(kJoinThreads)
+gdr_join_kernel(const __grid_constant__ Joins prm)
+{
+    extern __shared__ __align__(16) float smj[];
+    float *sS = smj + 2 * kD * kLdM;                 // [k][column]
+    const GdrArgs &a = prm.a;
+    const Item it = prm.items[blockIdx.x / a.H];
+    const int h = blockIdx.x % a.H, tid = threadIdx.x, c = 2 * (tid & 7), r = tid >> 3;   // rows r + 32 i
+    const int col = blockIdx.y * kJoinCols + c, P = it.parts;
+    const int len = max(min(a.cu[it.seq + 1], a.total_tokens) - max(a.cu[it.seq], 0), 0), seg = segment_of(len, P);
+    auto buffer = [&](int b) { return prm.ws + ((size_t)(it.buf + b) * a.H + h) * kD * kD; };
+    auto at = [&](float *p, int i) { return (float2 *)(p + (size_t)(r + 32 * i) * kD + col); };
+    // Segments 1 .. last + 1 have tokens: S_2 .. S_{last + 1} are formed, with M_1 .. M_last.
+    const int last = seg > 0 ? min(P - 2, (len - 1) / seg - 1) : 0;
+    auto fetch = [&](int p) {
+        const float *M = buffer(P - 1 + p);
+        const uint32_t to = smem_u32(smj + (p & 1) * kD * kLdM);
+        for (int e = tid; e < kD * kD / 4; e += kJoinThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         ::"r"(to + (e / 32 * kLdM + e % 32 * 4) * 4), "l"(M + 4 * e) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (last >= 1) fetch(1);
+    const int src = a.src ? a.src[it.seq] : -1;
+    if (a.state && src >= 0 && src < a.pool_size) {
+        float *row = a.state + ((size_t)src * a.H + h) * kD * kD;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *at(buffer(0), i) = *at(row, i);
+    }
+    if (last < 1) return;
+    float2 S[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[i] = *at(buffer(1), i);
+    for (int p = 1; p <= last; ++p) {
+        __syncthreads();                             // S and M_{p - 1} are no longer read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *(float2 *)&sS[(r + 32 * i) * kJoinCols + c] = S[i];
+            S[i] = *at(buffer(1 + p), i);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        if (p < last) fetch(p + 1);
+        const float *M = smj + (p & 1) * kD * kLdM + r * kLdM;
+#pragma unroll 4
+        for (int k = 0; k < kD; k += 4) {
+            float2 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = *(const float2 *)&sS[(k + u) * kJoinCols + c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 m = *(const float4 *)&M[32 * i * kLdM + k];
+                S[i] = __ffma2_rn(make_float2(m.x, m.x), x[0], S[i]);
+                S[i] = __ffma2_rn(make_float2(m.y, m.y), x[1], S[i]);
+                S[i] = __ffma2_rn(make_float2(m.z, m.z), x[2], S[i]);
+                S[i] = __ffma2_rn(make_float2(m.w, m.w), x[3], S[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *at(buffer(1 + p), i) = S[i];
+    }
+}
+
+// Segments of at most `chunks` chunks, for a sequence of n of them.
+int parts_of(int n, int chunks) { return n > chunks ? (n + chunks - 1) / chunks : 1; }
+bool may_split(const GdrArgs &a) { return (int64_t)a.H * (a.num_seqs + 1) <= kSms && a.total_tokens >= kMinSplit; }
+
+// The segment size (in chunks) of the split that ends first, or 0 where whole sequences do.  Both
+// launches fit the device once.  Without host offsets the lengths are taken as equal.
+int plan_split(const GdrArgs &a)
+{
+    if (!may_split(a)) return 0;
+    int lens[kSms], longest = 0;
+    for (int n = 0; n < a.num_seqs; ++n) {
+        const int64_t L = a.cu_host ? a.cu_host[n + 1] - a.cu_host[n] : (a.total_tokens + a.num_seqs - 1) / a.num_seqs;
+        lens[n] = (int)((L + kC - 1) / kC);
+        longest = lens[n] > longest ? lens[n] : longest;
+    }
+    auto fits = [&](int chunks) {
+        int64_t first = 0, all = 0;
+        for (int n = 0; n < a.num_seqs; ++n) {
+            const int P = parts_of(lens[n], chunks);
+            if (P > kMaxParts) return false;
+            first += P > 1 ? 2 * P - 3 : 0;
+            all += P;
+        }
+        return first * a.H <= kSms && all * a.H <= kSms;
+    };
+    int lo = 1, hi = longest;      // fits(hi): whole sequences
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (fits(mid)) hi = mid; else lo = mid + 1;
+    }
+    // In chunks (3.15 us): both passes, a join per segment, and the two more launches.  32 heads over
+    // one sequence of 4096 tokens: 179 us in 3 segments, 216 us whole; 2 heads over 40000: 254 us in
+    // 38, 1946 us whole; 1 head over 4096: 223 us in 64 segments, 94 us in 11, 214 us whole; 16 heads over 1100: 62
+    // us in 3, 71 us whole.
+    int best = 0, cost = longest;
+    for (int P = parts_of(longest, hi); P > 1; --P) {
+        const int chunks = (longest + P - 1) / P, c = 2 * chunks + P + kSplitCost;
+        if (c < cost) { best = chunks; cost = c; }
+    }
+    return best;
+}
+
 }  // namespace
 
-cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream)
+size_t gdr_tensor_core_workspace(int32_t total_tokens, int32_t num_seqs, int32_t H)
+{
+    GdrArgs a{};
+    a.total_tokens = total_tokens;
+    a.num_seqs = num_seqs;
+    a.H = H;
+    // Of a sequence's 2 P - 2 buffers per head all but one belong to a CTA of the first launch.
+    return may_split(a) ? (size_t)2 * kSms * kD * kD * sizeof(float) : 0;
+}
+
+cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream_t stream)
 {
     const int64_t ctas = (int64_t)a.num_seqs * a.H;
     if (a.dk != kD || a.dv != kD || !a.bf16 || !a.cu || ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -967,11 +1143,44 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, cudaStream_t stream)
         (!tc_rows_map(&mq, a.q, a.total_tokens, a.Hk) || !tc_rows_map(&mk, a.k, a.total_tokens, a.Hk) ||
          !tc_rows_map(&mv, a.v, a.total_tokens, a.H)))
         return cudaErrorInvalidValue;
-    // Longest sequences first (they set the end of the launch); the host offsets only
-    // order the CTAs, each of which reads its own bounds on the device.
     Params p;
     memset(&p, 0, sizeof(p));
     p.a = a;
+    if (const int chunks = plan_split(a)) {
+        Joins joins;
+        memset(&joins, 0, sizeof(joins));
+        joins.a = a;
+        joins.ws = p.ws = (float *)workspace;
+        p.split = true;
+        Params first = p;
+        int all = 0, firsts = 0, splits = 0, buf = 0;
+        for (int n = 0; n < a.num_seqs; ++n) {
+            const int64_t L = a.cu_host ? a.cu_host[n + 1] - a.cu_host[n] : (a.total_tokens + a.num_seqs - 1) / a.num_seqs;
+            const int P = parts_of((int)((L + kC - 1) / kC), chunks);
+            Item it = {(uint16_t)n, (uint16_t)buf, 0, (uint8_t)P, kOutputs};
+            for (int s = 0; s < P; ++s) {
+                it.part = (uint8_t)s;
+                it.kind = kOutputs;
+                p.items[all++] = it;
+                if (s + 1 == P) break;
+                it.kind = kOffset;
+                first.items[firsts++] = it;
+                it.kind = kMap;
+                if (s > 0) first.items[firsts++] = it;
+            }
+            if (P == 1) continue;
+            joins.items[splits++] = it;
+            buf += 2 * P - 2;
+        }
+        err = cudaFuncSetAttribute(gdr_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinSmem);
+        if (err != cudaSuccess) return err;
+        gdr_chunk_kernel<<<firsts * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, first);
+        gdr_join_kernel<<<dim3(splits * a.H, kD / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(joins);
+        gdr_chunk_kernel<<<all * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, p);
+        return cudaGetLastError();
+    }
+    // Longest sequences first (they set the end of the launch); the host offsets only
+    // order the CTAs, each of which reads its own bounds on the device.
     if (a.cu_host && a.num_seqs > 1 && a.num_seqs <= kGdrMaxOrder) {
         p.ordered = true;
         for (int i = 0; i < a.num_seqs; ++i) {     // insertion by length, ties by index

@@ -674,3 +674,72 @@ def test_binding_checks_shapes(K):
             K.kda_gdr_decode(**{**args, **kw})
     with pytest.raises(K.KdaError):       # fewer rows than sequences, none named
         K.kda_gdr_decode(**{**args, "state": st})
+
+
+SPLITS = [([1100], 2), ([2000], 16), ([1030, 1, 0, 700], 3), ([1500, 1400], 8), ([3300], 1)]
+
+
+@pytest.mark.parametrize("lens,H", SPLITS, ids=str)
+@pytest.mark.parametrize("block", [0, 128])
+def test_prefill_few_chains(K, lens, H, block):
+    """Long sequences of few heads, divided along their length: outputs, last rows and block
+    rows as ever, with and without the host's offsets, in place, with heads of every decay."""
+    N, T = len(lens), sum(lens)
+    ctx = [37 * n for n in range(N)]
+    x = U.tokens((T + 9,), 1, H, 128, 128, torch.bfloat16, seed=T, rate=(1e-4, 2.0))
+    cols = max((c + n) // 128 for c, n in zip(ctx, lens)) + 1
+    state = U.pool(2 * N + N * cols, H, 128, 128, seed=90)
+    table = torch.arange(2 * N, 2 * N + N * cols, dtype=torch.int32).view(N, cols) if block else None
+    src = [n if n != 1 else -1 for n in range(N)]
+    for dst in ([N + n for n in range(N)], list(range(N))):      # other rows; in place
+        if dst[0] == 0 and block:                                # and a block's row is the one read
+            table[0, (ctx[0] + lens[0]) // 128 - 1] = 0
+            dst[0] = -1
+        for host, pad in ((True, 0), (False, 9)):
+            y = x if pad else {n: t[:T].contiguous() for n, t in x.items()}
+            check_prefill(K, y, lens, H, state, src, dst, 0.5, "bf16", "tensor_core", ctx=ctx, table=table,
+                          block=block, host=host, pad=pad)
+
+
+def test_prefill_few_chains_shorter_on_the_device(K):
+    """Segments are planned from the host's lengths; the device's decide."""
+    cap, H = 4000, 2
+    x = U.tokens((cap,), 1, H, 128, 128, torch.bfloat16, seed=91)
+    d, state = dev(x), U.pool(2, H, 128, 128, seed=92)
+    for L in (0, 1, 64, 65, 700, 2049, 4000):
+        o, st = torch.full_like(d["v"], 7.0), state.cuda()
+        K.kda_gdr_prefill(d["q"], d["k"], d["v"], d["g"], d["beta"], i32([0, L]), state=st,
+                          src_slots=i32([0]), dst_slots=i32([1]), o=o)
+        ref_o, ref_S = U.reference(x, [(0, L)], H, 1.0, state, [0], [1])
+        assert U.max_err(o[:L], ref_o[:L]) <= TOL_TC and bool((o[L:] == 7.0).all())
+        assert U.max_err(st, ref_S) <= TOL_TC_S
+    assert K.kda_device_status() == 0
+
+
+def test_prefill_few_chains_nan_and_infinity_stay_in_their_columns(K):
+    """An infinity in v spoils its column from its token on, across segments, and no other."""
+    x = U.tokens((2500,), 1, 2, 128, 128, torch.bfloat16, seed=93)
+    y = {n: t.clone() for n, t in x.items()}
+    y["v"][300, 1, 5], y["v"][1700, 0, 9] = float("inf"), float("nan")
+    state = U.pool(2, 2, 128, 128, seed=94)
+    a, Sa = run_prefill(K, x, [2500], state, [0], [1], "tensor_core", 1.0)
+    b, Sb = run_prefill(K, y, [2500], state, [0], [1], "tensor_core", 1.0)
+    bad = torch.zeros_like(a, dtype=torch.bool)
+    bad[256:, 1, 5], bad[1600:, 0, 9] = True, True
+    assert torch.equal(a[~bad], b[~bad])
+    assert not bool(torch.isfinite(b[1900:, 1, 5]).any()) and not bool(torch.isfinite(b[1900:, 0, 9]).any())
+    ok = torch.ones(2, 128, 128, dtype=torch.bool)
+    ok[1, :, 5], ok[0, :, 9] = False, False
+    assert torch.equal(Sa[1].cpu()[ok], Sb[1].cpu()[ok])
+
+
+def test_prefill_workspace_is_checked(K):
+    x = dev(U.tokens((2000,), 1, 1, 128, 128, torch.bfloat16, seed=95))
+    cu = i32([0, 2000])
+    need = K.kda_gdr_prefill_workspace_size(2000, 1, 1, 1, 128, 128)
+    assert need > 0 and K.kda_gdr_prefill_workspace_size(2000, 1, 1, 1, 128, 128, algo="cuda_core") == 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    a = K.kda_gdr_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, workspace=ws)
+    ws.fill_(0xFF)             # (NaN) nothing is kept there between calls
+    b = K.kda_gdr_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, workspace=ws)
+    assert torch.equal(a, b)
