@@ -145,7 +145,7 @@ constexpr int kSplitCost = 3;                        // of the two more launches
 struct Params {
     GdrArgs a;
     float *ws;
-    bool ordered, split;
+    bool ordered;
     union {
         uint16_t order[kGdrMaxOrder];   // sequence of launch position i, longest first
         Item items[kSms];               // of launch position i, in a split
@@ -322,6 +322,9 @@ __device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// SPLIT: the launches over segments (their few more values in registers cost 3 % where there are
+// none: 3.16 and 3.07 us a chunk).
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params prm)
@@ -336,34 +339,41 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pos = blockIdx.x / a.H, h = blockIdx.x % a.H, hk = h / (a.H / a.Hk);
     Item it = {0, 0, 0, 1, kOutputs};
-    if (prm.split) it = prm.items[pos];
-    const int n = prm.split ? it.seq : prm.ordered ? prm.order[pos] : pos;
+    if (SPLIT) it = prm.items[pos];
+    const int n = SPLIT ? it.seq : prm.ordered ? prm.order[pos] : pos;
     int tbeg = max(a.cu[n], 0), len = max(min(a.cu[n + 1], a.total_tokens) - tbeg, 0);
     // This segment; those behind the sequence's end (the host's lengths may differ) do nothing.
-    const int seg = segment_of(len, it.parts), from = min((int64_t)len, (int64_t)it.part * seg);
-    const bool final = len - from <= seg;
-    if (it.part > 0 && from == len || it.kind != kOutputs && final) return;
-    tbeg += from;
-    len = final ? len - from : seg;
+    int from = 0;
+    bool final = true;
+    if (SPLIT) {
+        const int seg = segment_of(len, it.parts);
+        from = (int)min((int64_t)len, (int64_t)it.part * seg);
+        final = len - from <= seg;
+        if (it.part > 0 && from == len || it.kind != kOutputs && final) return;
+        tbeg += from;
+        len = final ? len - from : seg;
+    }
     const int64_t before = (int64_t)(a.ctx ? max(a.ctx[n], 0) : 0) + from;   // tokens before this segment
-    const int src = a.src ? a.src[n] : -1, dst = a.dst ? a.dst[n] : -1;
+    int src = a.src ? a.src[n] : -1, dst = final && a.dst ? a.dst[n] : -1;
+    if (!a.state || src < 0 || src >= a.pool_size) src = -1;
+    if (!a.state || dst < 0 || dst >= a.pool_size) dst = -1;
     auto row_of = [&](int slot) { return a.state + ((size_t)slot * a.H + h) * kD * kD; };
     auto buffer = [&](int b) { return prm.ws + ((size_t)(it.buf + b) * a.H + h) * kD * kD; };
-    const float *Sin = nullptr;                      // nullptr: zeros, or the identity
-    float *Sout = nullptr;
-    if (it.part > 0)
-        Sin = it.kind == kOutputs ? buffer(it.part) : nullptr;
-    else if (a.state && src >= 0 && src < a.pool_size)
-        Sin = prm.split && it.parts > 1 && it.kind == kOutputs ? buffer(0) : row_of(src);
-    if (it.kind != kOutputs)
-        Sout = buffer(it.kind == kMap ? it.parts - 1 + it.part : 1 + it.part);
-    else if (final && a.state && dst >= 0 && dst < a.pool_size)
-        Sout = row_of(dst);
+    // The state before this segment (nullptr: zeros, or the identity) and where the one after it goes.
+    auto state_in = [&]() -> const float * {
+        if (SPLIT && it.part > 0) return it.kind == kOutputs ? buffer(it.part) : nullptr;
+        if (src < 0) return nullptr;
+        return SPLIT && it.parts > 1 && it.kind == kOutputs ? buffer(0) : row_of(src);
+    };
+    auto state_out = [&]() -> float * {
+        if (SPLIT && it.kind != kOutputs) return buffer(it.kind == kMap ? it.parts - 1 + it.part : 1 + it.part);
+        return dst >= 0 ? row_of(dst) : nullptr;
+    };
 
     if (len == 0) {   // the state passes through
-        if (Sout && Sout != Sin) {
-            float4 *to = (float4 *)Sout;
-            const float4 *from = (const float4 *)Sin;
+        float4 *to = (float4 *)state_out();
+        const float4 *from = (const float4 *)state_in();
+        if (to && to != from) {
 #pragma unroll 1
             for (int e = tid; e < kD * kD / 4; e += kThreads)
                 to[e] = from ? from[e] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -425,7 +435,9 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp < kIntraWarp) {
         // ------------------------------------------------------------- chain --
         const int j = tid & 127, hh = warp >> 2;   // value channel; quarter of tokens / key channels
-        const bool map = it.kind == kMap;
+        const bool map = SPLIT && it.kind == kMap;
+        const float *S0 = state_in();
+        if (S0) S0 += (size_t)(32 * hh) * kD + j;
         // 16 columns of an accumulator as two bf16 operands of 8 columns each.
         auto put16 = [&](const float (&x)[16], uint32_t hi, uint32_t lo) {
             float h[8], l[8];
@@ -451,8 +463,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const float f = infos[0].in;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int row = 32 * hh + 16 * p + i;
-                x[i] = Sin ? Sin[(size_t)row * kD + j] * f : map && row == j ? f : 0.f;
+                x[i] = S0 ? S0[(size_t)(16 * p + i) * kD] * f : map && 32 * hh + 16 * p + i == j ? f : 0.f;
             }
             tmem_st16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
             put16(x, kTSb + 16 * hh + 8 * p, kTSb + 64 + 16 * hh + 8 * p);
@@ -525,7 +536,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (row >= 0 || last) {   // rows that keep the state after this chunk
 #pragma unroll 1
                 for (int w = 0; w < 4; ++w) {
-                    float *to = w >= 2 ? (last ? Sout : nullptr) : row >= 0 ? row_of(row) : nullptr;
+                    float *to = w >= 2 ? (last ? state_out() : nullptr) : row >= 0 ? row_of(row) : nullptr;
                     const int p = w & 1;
                     if (!to) continue;
                     tmem_ld16f(tmem_addr(tb, lq, kTS + 32 * hh + 16 * p), x);
@@ -717,7 +728,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             next_stage();
             const Info &in = infos[c % kInfos];
             const bool last = in.last != 0;
-            const int rows = it.kind == kOutputs ? in.len : 0;
+            const int rows = !SPLIT || it.kind == kOutputs ? in.len : 0;
             tc_fence_after_sync();
             // 16 tokens at a time: four 8 x 8 blocks (channels x tokens) become eight token rows of 32
             // channels, 16-byte pieces swizzled by token pair; a lane then stores two of them.
@@ -915,7 +926,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int start = 0;
         // Tokens left in the current block, and its index (no blocks: more than there are).
         int to_block = a.block > 0 ? a.block - (int)(before % a.block) : 0x7fffffff;
-        int64_t blk = a.block > 0 ? before / a.block : 0;
+        int blk = a.block > 0 ? (int)(before / a.block) : 0;
         // g and beta of tokens 2 lane, 2 lane + 1 of this chunk, and of the next if this one is full.
         float g[2], be[2], gn[2], bn[2];
         auto fetch = [&](int from, float (&g)[2], float (&be)[2]) {
@@ -976,7 +987,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 in.len = m;
                 in.last = start + m >= len;
                 in.row = -1;
-                if (a.block > 0 && it.kind == kOutputs && m == to_block && blk < a.table_cols) {
+                if (a.block > 0 && (!SPLIT || it.kind == kOutputs) && m == to_block && blk < a.table_cols) {
                     const int row = a.table[(size_t)n * a.table_cols + blk];
                     if (row >= 0 && row < a.pool_size) in.row = row;
                 }
@@ -1134,8 +1145,7 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
     const int64_t ctas = (int64_t)a.num_seqs * a.H;
     if (a.dk != kD || a.dv != kD || !a.bf16 || !a.cu || ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (ctas == 0) return cudaSuccess;
-    cudaError_t err = cudaFuncSetAttribute(gdr_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (err != cudaSuccess) return err;
+    cudaError_t err;
     CUtensorMap mq, mk, mv;
     memset(&mq, 0, sizeof(mq));
     mk = mv = mq;   // with no tokens no tile is read
@@ -1151,7 +1161,6 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
         memset(&joins, 0, sizeof(joins));
         joins.a = a;
         joins.ws = p.ws = (float *)workspace;
-        p.split = true;
         Params first = p;
         int all = 0, firsts = 0, splits = 0, buf = 0;
         for (int n = 0; n < a.num_seqs; ++n) {
@@ -1172,11 +1181,13 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
             joins.items[splits++] = it;
             buf += 2 * P - 2;
         }
+        err = cudaFuncSetAttribute(gdr_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (err != cudaSuccess) return err;
         err = cudaFuncSetAttribute(gdr_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinSmem);
         if (err != cudaSuccess) return err;
-        gdr_chunk_kernel<<<firsts * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, first);
+        gdr_chunk_kernel<true><<<firsts * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, first);
         gdr_join_kernel<<<dim3(splits * a.H, kD / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(joins);
-        gdr_chunk_kernel<<<all * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, p);
+        gdr_chunk_kernel<true><<<all * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, p);
         return cudaGetLastError();
     }
     // Longest sequences first (they set the end of the launch); the host offsets only
@@ -1195,7 +1206,9 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
             p.order[at] = (uint16_t)i;
         }
     }
-    gdr_chunk_kernel<<<(unsigned)ctas, kThreads, kSmem, stream>>>(mq, mk, mv, p);
+    err = cudaFuncSetAttribute(gdr_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err != cudaSuccess) return err;
+    gdr_chunk_kernel<false><<<(unsigned)ctas, kThreads, kSmem, stream>>>(mq, mk, mv, p);
     return cudaGetLastError();
 }
 
