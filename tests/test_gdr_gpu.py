@@ -743,3 +743,17 @@ def test_prefill_workspace_is_checked(K):
     ws.fill_(0xFF)             # (NaN) nothing is kept there between calls
     b = K.kda_gdr_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, workspace=ws)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("block", [0, 64])
+def test_prefill_a_few_tokens_each(K, block):
+    """Sequences of no, one and a few tokens beside longer ones, at and across block ends."""
+    lens, ctx = [1, 3, 2, 0, 4, 5, 70, 1, 3, 2], [63, 62, 64, 10, 60, 0, 3, 0, 127, 126]
+    N, H = len(lens), 3
+    x = U.tokens((sum(lens),), 1, H, 128, 128, torch.bfloat16, seed=96)
+    state = U.pool(2 * N + 3 * N, H, 128, 128, seed=97)
+    table = torch.arange(2 * N, 5 * N, dtype=torch.int32).view(N, 3) if block else None
+    src = [n if n != 2 else -1 for n in range(N)]
+    for dst in ([N + n for n in range(N)], list(range(N))):
+        for algo in algos_for("bf16", 128, 128):
+            check_prefill(K, x, lens, H, state, src, dst, 0.5, "bf16", algo, ctx=ctx, table=table, block=block)
