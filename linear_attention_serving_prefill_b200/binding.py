@@ -523,21 +523,25 @@ def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, bloc
         raise ValueError("total_tokens must not be negative")
     if out is None:
         # One allocation for the int32 outputs, padded so that the positions are 16-byte aligned.
-        pad = -(3 * N + 2) % 4
-        cu, src, dst, head, _, pos = torch.empty(
-            3 * N + 2 + pad + total_tokens, dtype=i32, device=new_lens.device).split_with_sizes(
-                (N + 1, N, N, 1, pad, total_tokens))
-        out = BlockPlan(cu, pos, torch.empty(total_tokens, dtype=torch.int64, device=new_lens.device),
-                        src, dst, head)
+        at = 3 * N + 2 + -(3 * N + 2) % 4
+        flat = torch.empty(at + total_tokens, dtype=i32, device=new_lens.device)
+        cu, src, dst, head, _, pos = flat.split_with_sizes((N + 1, N, N, 1, at - 3 * N - 2, total_tokens))
+        slots = torch.empty(total_tokens, dtype=torch.int64, device=new_lens.device)
+        out = BlockPlan(cu, pos, slots, src, dst, head)
+        p = flat.data_ptr()
+        cu, src, dst, head, pos, slots = (p, p + 4 * (N + 1), p + 4 * (2 * N + 1), p + 4 * (3 * N + 1),
+                                          p + 4 * at, slots.data_ptr())
+    else:
+        cu = _ptr(out.cu_seqlens, "cu_seqlens", i32, dev, (N + 1,))
+        pos = _ptr(out.positions, "positions", i32, dev, (total_tokens,))
+        slots = _ptr(out.token_slots, "token_slots", torch.int64, dev, (total_tokens,))
+        src = _ptr(out.src_slots, "src_slots", i32, dev, (N,))
+        dst = _ptr(out.dst_slots, "dst_slots", i32, dev, (N,))
+        head = _ptr(out.free_head, "free_head", i32, dev, (1,))
     _call(_lib.kda_block_plan, "kda_block_plan", dev, stream,
           _ptr(new_lens, "new_lens", i32, dev, (N,)), _ptr(ctx_lens, "ctx_lens", i32, dev, (N,)),
           N, _ptr(free_blocks, "free_blocks", i32, dev, (F,)), F,
           _ptr(free_head, "free_head", i32, dev, (1,)),
           _ptr(block_table, "block_table", i32, dev), block_table.shape[1], block_size,
-          total_tokens, _ptr(out.cu_seqlens, "cu_seqlens", i32, dev, (N + 1,)),
-          _ptr(out.positions, "positions", i32, dev, (total_tokens,)),
-          _ptr(out.token_slots, "token_slots", torch.int64, dev, (total_tokens,)),
-          _ptr(out.src_slots, "src_slots", i32, dev, (N,)),
-          _ptr(out.dst_slots, "dst_slots", i32, dev, (N,)),
-          _ptr(out.free_head, "free_head", i32, dev, (1,)))
+          total_tokens, cu, pos, slots, src, dst, head)
     return out
