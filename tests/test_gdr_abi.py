@@ -97,6 +97,21 @@ def test_workspace_size_is_defined_for_every_call():
     assert B._lib.kda_gdr_prefill_workspace_size(100, 2, 3, 4, 128, 128, BF16, AUTO) == 0
 
 
+def test_workspace_where_long_sequences_may_be_divided():
+    """Few (sequence, head) pairs with many tokens need a workspace; a call without it, or with
+    a smaller one, is refused before any launch."""
+    need = B.kda_gdr_prefill_workspace_size(5000, 1, 1, 2, 128, 128)
+    assert need > 0
+    assert B.kda_gdr_prefill_workspace_size(5000, 1, 1, 148, 128, 128) == 0
+    assert B.kda_gdr_prefill_workspace_size(500, 1, 1, 2, 128, 128) == 0
+    assert B.kda_gdr_prefill_workspace_size(5000, 1, 1, 2, 64, 64) == 0
+    assert B.kda_gdr_prefill_workspace_size(5000, 1, 1, 2, 128, 128, torch.float32) == 0
+    one = dict(N=1, T=5000, Hk=1, H=2)
+    assert prefill(**one) == WORKSPACE
+    assert prefill(**one, ws=P, ws_bytes=need - 1) == WORKSPACE
+    assert prefill(**one, ws=P + 8, ws_bytes=need) == INVALID
+
+
 def test_binding_refuses_host_tensors():
     x = U.tokens((4,), 1, 2, 32, 32, torch.float32, seed=0)
     cu = torch.tensor([0, 4], dtype=torch.int32)
