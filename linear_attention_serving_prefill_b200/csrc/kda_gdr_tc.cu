@@ -41,7 +41,7 @@
 //   info  (warp 31)      chunk bounds and factors (a warp scan).
 // K and Q are loaded twice (the second time from L2): A and P are formed up to three chunks
 // ahead of the state, and a tile that stayed for both uses would sit idle in between.
-// One chain takes 3.1 us a chunk alone and 3.15 us at 96 CTAs (32768 tokens x 96 heads: 1.61 ms):
+// One chain takes 3.05 us a chunk alone and 3.1 us at 96 CTAs (32768 tokens x 96 heads: 1.60 ms):
 // the state's way through three products and three passes of the chain warps, about 6000 cycles,
 // next to the other roles, which take as long (A and P wait for one accumulator).  Tried and
 // slower: fewer, wider chain warps; register splits between roles; deeper tile rings in place of
@@ -326,8 +326,13 @@ __device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
 }
 
 // SPLIT: the launches over segments (their few more values in registers cost 3 % where there are
-// none: 3.16 and 3.07 us a chunk).
-template <bool SPLIT>
+// none: 3.16 and 3.07 us a chunk).  COMPACT: for launches that fill the device, whose SMs wait for
+// instructions (a cache line per 2.1 cycles and GPC at 148 CTAs): the inverse's substitution as a
+// loop, longer by 600 cycles and shorter by 3 KB.  us a chunk with it / without, at 96, 112, 120,
+// 136 and 148 CTAs: 3.47 / 3.20, 3.47 / 3.27, 3.48 / 3.56 (another device 3.48 / 3.23), 3.64 / 3.96,
+// 3.61 / 3.93.
+constexpr int kCompactCtas = 129;
+template <bool SPLIT, bool COMPACT>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params prm)
@@ -646,7 +651,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // fp32, P to its operand.
             uint8_t *img = sm + kOffP + stage * 8192;
 #pragma unroll 1
-            for (int s0 = 0; s0 < 32 * (1 + half); s0 += 16) {
+            for (int k = 0; k < 2 * (1 + half); ++k) {
+                const int s0 = (32 * half + 16 * k) & 63;   // the diagonal blocks first
                 // Last column kept (15 or more: all; none in rows past the last token).
                 const int lim = (r >= in.len ? -1 : is_p ? r : r - 1) - s0;
                 float v[16];
@@ -678,17 +684,21 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             m[kMLow / 16 + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
                         }
                     }
+                    if (k == 1) {          // the inverses may start
+                        __threadfence_block();
+                        asm volatile("barrier.arrive %0, 128;" ::"r"(3 + group) : "memory");
+                    }
                 }
             }
             if (is_p) fence_proxy_async_smem();
             tc_fence_before_sync();
             mbar_arrive(&bars.ap_tfree);
-            if (group_sync_any(group, !ok)) break;
             // Inverse of the two 32 x 32 diagonal blocks, one warp each (those of P, whose readback is
             // shorter; on the warps of A 3.16 instead of 3.11 us/chunk at 96 heads): half a warp
             // solves a 16 x 16 block, lane j its column j, four unknowns at a time; then the block
             // between them.
             if (is_p) {
+                asm volatile("barrier.sync %0, 128;" ::"r"(3 + group) : "memory");
                 uint8_t *Tw = tt + half * kMTT;
                 const int sub = lane >> 4;
                 const float *B = diag + (2 * half + sub) * (kMDiag / 4);
@@ -696,26 +706,49 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+                if constexpr (COMPACT) {   // x: rows m0 .. m0 + 15; those past the block's last are never used
+                    // Transposed: lane j's column is row j of the block.
+                    uint8_t *p = Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub);
+#pragma unroll 1
+                    for (int m0 = 0; m0 < 16; m0 += 4, B += 4 * kLdB + 4, p += 8) {
 #pragma unroll
-                for (int m0 = 0; m0 < 16; m0 += 4) {
+                        for (int i = 1; i < 16; ++i) {
+                            const float4 l = *(const float4 *)&B[i * kLdB];
+                            const float lv[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-                    for (int i = m0 + 1; i < 16; ++i) {
-                        const float4 l = *(const float4 *)&B[i * kLdB + m0];
-                        const float lv[4] = {l.x, l.y, l.z, l.w};
+                            for (int m = 0; m < 4; ++m)
+                                if (m < i) x[i] = fmaf(-lv[m], x[m], x[i]);
+                        }
+                        uint32_t hi[2], lo[2];
 #pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
+                        for (int u = 0; u < 2; ++u) split_half(x[2 * u], x[2 * u + 1], hi[u], lo[u]);
+                        *(uint2 *)p = make_uint2(hi[0], hi[1]);
+                        *(uint2 *)(p + kMLow) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+                        for (int i = 0; i < 12; ++i) x[i] = x[i + 4];
                     }
-                }
-                // Transposed: lane j's column is row j of the block.
-                uint4 *p = (uint4 *)(Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub));
+                } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t hi[4], lo[4];
+                    for (int m0 = 0; m0 < 16; m0 += 4) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) split_half(x[8 * i + 2 * u], x[8 * i + 2 * u + 1], hi[u], lo[u]);
-                    p[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    p[kMLow / 16 + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int i = m0 + 1; i < 16; ++i) {
+                            const float4 l = *(const float4 *)&B[i * kLdB + m0];
+                            const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
+                        }
+                    }
+                    // Transposed: lane j's column is row j of the block.
+                    uint4 *p = (uint4 *)(Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) split_half(x[8 * i + 2 * u], x[8 * i + 2 * u + 1], hi[u], lo[u]);
+                        p[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        p[kMLow / 16 + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
                 __syncwarp();
                 float z[2][4];
@@ -747,7 +780,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             // The diagonal blocks: half a block per warp, eight rows i at a time; tiles of T^T are
             // columns j of the image in blocks of eight.
-#pragma unroll
+#pragma unroll(COMPACT ? 1 : 2)
             for (int u = 0; u < 2; ++u) {
                 const int i = (is_p ? 16 : 0) + 8 * u;
                 const uint32_t tw = smem_u32(tt + half * kMTT) + 2 * (lane * kLdT + i);
@@ -1188,6 +1221,17 @@ int plan_split(const GdrArgs &a)
 
 }  // namespace
 
+template <bool SPLIT>
+static cudaError_t launch_chunks(int ctas, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                                 const Params &p, cudaStream_t stream)
+{
+    auto *kernel = ctas >= kCompactCtas ? gdr_chunk_kernel<SPLIT, true> : gdr_chunk_kernel<SPLIT, false>;
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err != cudaSuccess) return err;
+    kernel<<<(unsigned)ctas, kThreads, kSmem, stream>>>(q, k, v, p);
+    return cudaGetLastError();
+}
+
 size_t gdr_tensor_core_workspace(int32_t total_tokens, int32_t num_seqs, int32_t H)
 {
     GdrArgs a{};
@@ -1239,14 +1283,13 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
             joins.items[splits++] = it;
             buf += 2 * P - 2;
         }
-        err = cudaFuncSetAttribute(gdr_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-        if (err != cudaSuccess) return err;
         err = cudaFuncSetAttribute(gdr_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinSmem);
         if (err != cudaSuccess) return err;
-        gdr_chunk_kernel<true><<<firsts * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, first);
+        err = launch_chunks<true>(firsts * a.H, mq, mk, mv, first, stream);
+        if (err != cudaSuccess) return err;
         gdr_join_kernel<<<dim3(splits * a.H, kD / kJoinCols), kJoinThreads, kJoinSmem, stream>>>(joins);
-        gdr_chunk_kernel<true><<<all * a.H, kThreads, kSmem, stream>>>(mq, mk, mv, p);
-        return cudaGetLastError();
+        err = cudaGetLastError();
+        return err == cudaSuccess ? launch_chunks<true>(all * a.H, mq, mk, mv, p, stream) : err;
     }
     // Longest sequences first (they set the end of the launch); the host offsets only
     // order the CTAs, each of which reads its own bounds on the device.
@@ -1264,10 +1307,7 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
             p.order[at] = (uint16_t)i;
         }
     }
-    err = cudaFuncSetAttribute(gdr_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (err != cudaSuccess) return err;
-    gdr_chunk_kernel<false><<<(unsigned)ctas, kThreads, kSmem, stream>>>(mq, mk, mv, p);
-    return cudaGetLastError();
+    return launch_chunks<false>((int)ctas, mq, mk, mv, p, stream);
 }
 
 }  // namespace kda
