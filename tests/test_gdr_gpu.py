@@ -757,3 +757,27 @@ def test_prefill_a_few_tokens_each(K, block):
     for dst in ([N + n for n in range(N)], list(range(N))):
         for algo in algos_for("bf16", 128, 128):
             check_prefill(K, x, lens, H, state, src, dst, 0.5, "bf16", algo, ctx=ctx, table=table, block=block)
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("bf16", 64, 32), ("f32", 32, 64)])
+def test_decode_more_states_than_fit_at_once(K, dtype, dk, dv):
+    """Several tokens each of more states than the device holds at once, of 0 .. Tq tokens, with
+    rows missing and states passed through."""
+    B, Tq, Hk, H = 60, 5, 6, 24
+    x = U.tokens((B * Tq,), Hk, H, dk, dv, DT[dtype], seed=98)
+    state = U.pool(2 * B, H, dk, dv, seed=99)
+    nt = [(3 * b) % (Tq + 1) for b in range(B)]
+    src = [b if b % 7 else -1 for b in range(B)]
+    dst = [B + b if b % 5 else (-1 if b % 2 else b) for b in range(B)]
+    d = {n: t.cuda().view(B, Tq, *t.shape[1:]) for n, t in x.items()}
+    ref_o, ref_S = U.reference(x, [(b * Tq, nt[b]) for b in range(B)], H, 0.7, state, src, dst)
+    live = torch.isfinite(ref_o)
+    ref_o = torch.where(live, ref_o, torch.full_like(ref_o, 7.0))
+    st, o = state.cuda(), torch.full_like(d["v"], 7.0)
+    K.kda_gdr_decode(d["q"], d["k"], d["v"], d["g"], d["beta"], st, src_slots=i32(src), dst_slots=i32(dst),
+                     num_tokens=i32(nt), scale=0.7, o=o)
+    flat = o.view(B * Tq, H, dv).cpu()
+    assert bool((flat[~live] == 7.0).all()) and U.max_err(flat, ref_o) <= TOL_O[dtype]
+    assert U.max_err(st, ref_S) <= TOL_F32
+    kept = [r for r in range(2 * B) if r not in dst]
+    assert torch.equal(st[kept].cpu(), state[kept])
