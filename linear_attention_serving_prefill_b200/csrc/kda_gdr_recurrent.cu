@@ -25,12 +25,14 @@
 //
 // A long sequence is bound by the latency of one token's chain (two reductions, their
 // shuffles and the update, one after the other): 0.31 us a token at dk = dv = 128, 0.25 us
-// at 64.  A verify pass (64 x 96 states of 128 x 128, 4 tokens, 403 MB) takes 122 us and a
-// replay (100 x 32 key heads, 96 heads, up to 6 tokens) 246 us, 3.3 and 5.2 TB/s: the steps'
-// shared-memory loads and shuffles, at the 16 warps per SM that the states leave room for.
+// at 64.  A verify pass (64 x 96 states of 128 x 128, 4 tokens, 403 MB) takes 118 us and a
+// replay (100 x 32 key heads, 96 heads, up to 6 tokens) 237 us, 3.4 and 5.4 TB/s: the steps'
+// shared-memory loads and shuffles, at the 16 warps per SM that the states leave room for (the
+// loads and stores alone: 72 and 205 us).
 // Slower, both measured: four tokens at a time from one pass over the state and a small
 // triangular solve (verify 119, replay 271 us, packed 0.38 us a token), and that with four
-// columns and half the rows per lane (115, 266 us, 0.42 us).
+// columns and half the rows per lane (115, 266 us, 0.42 us); the same products on m16n8k16 warp
+// instructions with S in three bf16 parts (119, 297 us).
 #include "kda_common.cuh"
 #include "kda_gdr.h"
 
@@ -301,13 +303,30 @@ gdr_recurrent_kernel(GdrArgs a)
     if (dst >= 0 && (len > 0 || dst != src)) S.store(row_of(dst));
 }
 
+// One of PARTS column parts of a sequence's state in the decode layout.
+struct Item { int n, h, part, src, dst, len; };
+template <int PARTS> __device__ __forceinline__ Item item_at(const GdrArgs &a, uint32_t it) {
+    Item x;
+    x.part = it % PARTS;
+    const uint32_t chain = it / PARTS;
+    x.n = chain / (uint32_t)a.H;
+    x.h = chain - x.n * a.H;
+    x.len = a.num_tokens ? min(max(a.num_tokens[x.n], 0), a.Tq) : a.Tq;
+    // Pool rows: outside [0, pool_size) the state starts from zero / is not written.
+    x.src = a.src ? a.src[x.n] : x.n;
+    x.dst = a.dst ? a.dst[x.n] : x.src;
+    if (x.src < 0 || x.src >= a.pool_size) x.src = -1;
+    if (!a.update || x.dst < 0 || x.dst >= a.pool_size || (x.len == 0 && x.dst == x.src)) x.dst = -1;
+    return x;
+}
+
 // A few tokens of each of many sequences.  A CTA walks over states; while it applies one
 // state's tokens, the next state's columns and tokens are on their way into shared memory
 // (cp.async; a thread fetches what it keeps, so the state needs no barrier), so that loads
 // and steps overlap although a state fills the registers.
 template <int DK, int DV, typename T>
 __global__ void __launch_bounds__(32 * kWarpsOf<DV>, 16 / kWarpsOf<DV>)
-gdr_few_kernel(GdrArgs a, int64_t items)
+gdr_few_kernel(GdrArgs a, uint32_t items)
 {
     using Cols = Columns<DK, DV>;
     constexpr int kWarps = kWarpsOf<DV>, kThreads = 32 * kWarps, kLd = Cols::kLd, R = Cols::R;
@@ -320,31 +339,17 @@ gdr_few_kernel(GdrArgs a, int64_t items)
     __shared__ float rG[kFew], rB[kFew], sA[kFew], sB[kFew], sKQ[kFew];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t group = a.H / a.Hk;
     const int rq = lane >> 3, own_col = 16 * warp + 2 * (lane & 7);
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v;
     T *o = (T *)a.o;
 
-    struct Item { int n, h, part, src, dst, len; };
-    auto item_at = [&](int64_t it) {
-        Item x;
-        x.part = (int)(it % kParts);
-        const int64_t chain = it / kParts;
-        x.n = (int)(chain / a.H);
-        x.h = (int)(chain - (int64_t)x.n * a.H);
-        x.len = a.num_tokens ? min(max(a.num_tokens[x.n], 0), a.Tq) : a.Tq;
-        // Pool rows: outside [0, pool_size) the state starts from zero / is not written.
-        x.src = a.src ? a.src[x.n] : x.n;
-        x.dst = a.dst ? a.dst[x.n] : x.src;
-        if (x.src < 0 || x.src >= a.pool_size) x.src = -1;
-        if (!a.update || x.dst < 0 || x.dst >= a.pool_size || (x.len == 0 && x.dst == x.src)) x.dst = -1;
-        return x;
-    };
     auto state_at = [&](const Item &x, int slot) {   // row 2 rq, this lane's column pair
         return a.state + ((size_t)slot * a.H + x.h) * DK * DV + (size_t)(2 * rq) * DV + x.part * kCols + own_col;
     };
     int buf = 0;                   // rV's half that the next copies go to
     auto fetch_tokens = [&](const Item &x, int base) {
-        const int hk = x.h / (a.H / a.Hk), m = min(kFew, x.len - base);
+        const int hk = (uint32_t)x.h / group, m = min(kFew, x.len - base);
         const size_t t0 = (size_t)x.n * a.Tq + base;
         for (int e = tid; e < m * (DK / kEl); e += kThreads) {
             const int t = e / (DK / kEl), c = (e % (DK / kEl)) * kEl;
@@ -374,13 +379,13 @@ gdr_few_kernel(GdrArgs a, int64_t items)
         fetch_tokens(x, 0);
     };
 
-    int64_t it = blockIdx.x;
-    Item x = item_at(it);          // (no more CTAs than items)
+    uint32_t it = blockIdx.x;
+    Item x = item_at<kParts>(a, it);          // (no more CTAs than items)
     fetch(x);
     for (;;) {
-        const bool more = it + gridDim.x < items;
+        const bool more = items - it > gridDim.x;
         Item next = x;
-        if (more) next = item_at(it + gridDim.x);
+        if (more) next = item_at<kParts>(a, it + gridDim.x);
         Cols S;
         S.run = 1.f;
         for (int base = 0; base == 0 || base < x.len; base += kFew) {
@@ -438,12 +443,12 @@ cudaError_t launch_typed(const GdrArgs &a, cudaStream_t stream)
     constexpr int kThreads = 32 * kWarpsOf<DV>;
     const int64_t items = (int64_t)a.num_seqs * a.H * (DV / (kThreads / 2));
     if (items == 0) return cudaSuccess;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (a.cu) {
-        if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
         gdr_recurrent_kernel<DK, DV, T><<<(unsigned)items, kThreads, 0, stream>>>(a);
     } else {
         const int64_t resident = (int64_t)kSms * (16 / kWarpsOf<DV>);
-        gdr_few_kernel<DK, DV, T><<<(unsigned)(items < resident ? items : resident), kThreads, 0, stream>>>(a, items);
+        gdr_few_kernel<DK, DV, T><<<(unsigned)(items < resident ? items : resident), kThreads, 0, stream>>>(a, (uint32_t)items);
     }
     return cudaGetLastError();
 }
