@@ -32,8 +32,8 @@
 //   chain (warps 0-15)   S^T K^T to R^T, F^T, and S^T times its factor, each from its
 //                        accumulator to two bf16 operands; the fp32 master;
 //   intra (warps 16-23)  two groups, even and odd chunks: A and P from the accumulator,
-//                        T by 16 x 16 forward substitution (fp32) and two block doublings
-//                        (warp products of split fp16), T's two bf16 operands;
+//                        T by forward substitution in 8 x 8 blocks (fp32) and three block
+//                        doublings (warp products of split fp16), T's two bf16 operands;
 //   aux   (warps 24-27)  O^T to o;
 //   issue (warp 28)      the products of the state chain;
 //   load  (warps 29, 30) the K and Q tiles for A and P and their product; K, Q and V for the
@@ -327,10 +327,9 @@ __device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
 
 // SPLIT: the launches over segments (their few more values in registers cost 3 % where there are
 // none: 3.16 and 3.07 us a chunk).  COMPACT: for launches that fill the device, whose SMs wait for
-// instructions (a cache line per 2.1 cycles and GPC at 148 CTAs): the inverse's substitution as a
-// loop, longer by 600 cycles and shorter by 3 KB.  us a chunk with it / without, at 96, 112, 120,
-// 136 and 148 CTAs: 3.47 / 3.20, 3.47 / 3.27, 3.48 / 3.56 (another device 3.48 / 3.23), 3.64 / 3.96,
-// 3.61 / 3.93.
+// instructions (a cache line per 2.1 cycles and GPC at 148 CTAs): the inverse's first step as a loop,
+// longer by 600 cycles and shorter by 1.4 KB.  us a chunk with it / without, at 96, 120, 128, 136
+// and 148 CTAs: 3.47 / 3.11, 3.48 / 3.24, 3.49 / 3.4, 3.64 / 3.8, 3.71 / 3.90.
 constexpr int kCompactCtas = 129;
 template <bool SPLIT, bool COMPACT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -694,20 +693,22 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_before_sync();
             mbar_arrive(&bars.ap_tfree);
             // Inverse of the two 32 x 32 diagonal blocks, one warp each (those of P, whose readback is
-            // shorter; on the warps of A 3.16 instead of 3.11 us/chunk at 96 heads): half a warp
-            // solves a 16 x 16 block, lane j its column j, four unknowns at a time; then the block
-            // between them.
+            // shorter; on the warps of A 3.16 instead of 3.11 us/chunk at 96 heads): four 8 x 8 blocks
+            // by substitution, then the blocks between them, 8 x 8 and 16 x 16.  COMPACT: the 16 x 16
+            // blocks by substitution, half a warp each, lane j its column j, four unknowns at a time.
             if (is_p) {
                 asm volatile("barrier.sync %0, 128;" ::"r"(3 + group) : "memory");
                 uint8_t *Tw = tt + half * kMTT;
-                const int sub = lane >> 4;
-                const float *B = diag + (2 * half + sub) * (kMDiag / 4);
-                const int j = lane & 15, g = lane >> 2, t = lane & 3;
-                float x[16];
+                const int g = lane >> 2, t = lane & 3;
+                if constexpr (COMPACT) {
+                    const int sub = lane >> 4;
+                    const float *B = diag + (2 * half + sub) * (kMDiag / 4);
+                    const int j = lane & 15;
+                    float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
-                if constexpr (COMPACT) {   // x: rows m0 .. m0 + 15; those past the block's last are never used
-                    // Transposed: lane j's column is row j of the block.
+                    for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+                    // x: rows m0 .. m0 + 15 (those past the block's last are never used); stored transposed,
+                    // lane j's column as row j of the block.
                     uint8_t *p = Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub);
 #pragma unroll 1
                     for (int m0 = 0; m0 < 16; m0 += 4, B += 4 * kLdB + 4, p += 8) {
@@ -727,30 +728,66 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 12; ++i) x[i] = x[i + 4];
                     }
+                    __syncwarp();
                 } else {
+                    const float *B = diag + 2 * half * (kMDiag / 4);       // its two 16 x 16 blocks
+                    {   // four 8 x 8 blocks, a column j per lane
+                        const int j = lane & 7, sub = lane >> 4, q = (lane >> 3) & 1;
+                        const float *L = B + sub * (kMDiag / 4) + 8 * q * (kLdB + 1);
+                        float x[8];
 #pragma unroll
-                    for (int m0 = 0; m0 < 16; m0 += 4) {
+                        for (int i = 0; i < 8; ++i) x[i] = i == j ? 1.f : 0.f;
 #pragma unroll
-                        for (int i = m0 + 1; i < 16; ++i) {
-                            const float4 l = *(const float4 *)&B[i * kLdB + m0];
-                            const float lv[4] = {l.x, l.y, l.z, l.w};
+                        for (int m0 = 0; m0 < 8; m0 += 4) {
 #pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
+                            for (int i = m0 + 1; i < 8; ++i) {
+                                const float4 l = *(const float4 *)&L[i * kLdB + m0];
+                                const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                                for (int m = 0; m < 4; ++m)
+                                    if (m0 + m < i) x[i] = fmaf(-lv[m], x[m0 + m], x[i]);
+                            }
                         }
-                    }
-                    // Transposed: lane j's column is row j of the block.
-                    uint4 *p = (uint4 *)(Tw + 2 * ((16 * sub + j) * kLdT + 16 * sub));
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                        // Transposed: lane j's column is row j of the block; left of a lower one zeros.
                         uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) split_half(x[8 * i + 2 * u], x[8 * i + 2 * u + 1], hi[u], lo[u]);
-                        p[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        p[kMLow / 16 + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int u = 0; u < 4; ++u) split_half(x[2 * u], x[2 * u + 1], hi[u], lo[u]);
+                        uint4 *p = (uint4 *)(Tw + 2 * ((16 * sub + 8 * q + j) * kLdT + 16 * sub));
+                        const uint4 zero = make_uint4(0, 0, 0, 0);
+                        if (q) p[0] = p[kMLow / 16] = zero;
+                        p[q] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        p[q + kMLow / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
+                    __syncwarp();
+                    {   // the blocks between them, both 16 x 16 at once: two diagonal tiles of each operand
+                        const uint32_t p = smem_u32(Tw) + 2 * ((lane & 7) * kLdT + ((lane >> 3) & 1) * (16 * kLdT + 16)) + (lane >> 4) * kMLow;
+                        uint32_t tj[4], ti[4], ah[2], al[2];     // (high, high, low, low) of the two blocks
+                        ldmatrix4<false>(p, tj);
+                        ldmatrix4<true>(p + 2 * 8 * (kLdT + 1), ti);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float2 l = *(const float2 *)&B[u * (kMDiag / 4) + (8 + g) * kLdB + 2 * t];
+                            split_half(l.x, l.y, ah[u], al[u]);
+                        }
+                        float v[4] = {}, z[4] = {};
+                        const uint32_t th[4] = {tj[0], 0, 0, tj[1]}, tl[4] = {tj[2], 0, 0, tj[3]};
+                        mma_f16(v, th, al[0], al[1]);
+                        mma_f16(v, tl, ah[0], ah[1]);
+                        mma_f16(v, th, ah[0], ah[1]);
+                        uint32_t vh[4] = {}, vl[4] = {};
+                        split_half(v[0], v[1], vh[0], vl[0]);
+                        split_half(v[2], v[3], vh[3], vl[3]);
+                        mma_f16(z, vh, ti[2], ti[3]);
+                        mma_f16(z, vl, ti[0], ti[1]);
+                        mma_f16(z, vh, ti[0], ti[1]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t *to = (uint32_t *)(Tw + 2 * ((16 * u + g) * kLdT + 16 * u + 8 + 2 * t));
+                            split_half(-z[2 * u], -z[2 * u + 1], to[0], to[kMLow / 4]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 float z[2][4];
                 const uint32_t tw = smem_u32(Tw);
                 block_product<16>(tw, tw + 2 * 16 * kLdT, tw + 2 * (16 * kLdT + 16), 0, 0, lane, z);
@@ -780,7 +817,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             // The diagonal blocks: half a block per warp, eight rows i at a time; tiles of T^T are
             // columns j of the image in blocks of eight.
-#pragma unroll(COMPACT ? 1 : 2)
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 const int i = (is_p ? 16 : 0) + 8 * u;
                 const uint32_t tw = smem_u32(tt + half * kMTT) + 2 * (lane * kLdT + i);

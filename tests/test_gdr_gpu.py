@@ -781,3 +781,12 @@ def test_decode_more_states_than_fit_at_once(K, dtype, dk, dv):
     assert U.max_err(st, ref_S) <= TOL_F32
     kept = [r for r in range(2 * B) if r not in dst]
     assert torch.equal(st[kept].cpu(), state[kept])
+
+
+def test_prefill_fills_the_device(K):
+    """As many (sequence, head) pairs as SMs, with ends inside every 16-token tile."""
+    lens, H = [77, 121, 150], 49
+    x = U.tokens((sum(lens),), 7, H, 128, 128, torch.bfloat16, seed=100)
+    state = U.pool(6, H, 128, 128, seed=101)
+    for algo in algos_for("bf16", 128, 128):
+        check_prefill(K, x, lens, H, state, [0, 1, 2], [3, 4, 5], 0.5, "bf16", algo)
