@@ -459,7 +459,8 @@ size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, in
  *                   sizes); KDA_ALGO_TENSOR_CORE_SPLIT is KDA_ERR_UNSUPPORTED.
  * The tensor-core path holds the state in fp32 and its operands in two bf16 numbers each
  * (state within 2e-5 of the recurrence in 64 bits, 2-norm; o rounded to bf16 after products
- * whose S and P are single bf16 numbers).  A NaN or an infinity in a token reaches its own
+ * whose S and P are single bf16 numbers), for keys with beta |k|^2 <= 2 (past it the
+ * recurrence itself grows from token to token) and |v| up to 2^20.  A NaN or an infinity in a token reaches its own
  * sequence and head, there from the start of the token's chunk of 64 on at the earliest.
  */
 kda_status kda_gdr_prefill(const void *q, const void *k, const void *v, const float *g,
