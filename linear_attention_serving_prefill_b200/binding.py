@@ -429,15 +429,10 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     dt = q.dtype
     if o is None:
         o = torch.empty_like(v)
-    need = _lib.kda_gdr_prefill_workspace_size(T, N, Hk, H, dk, dv, KDA_DTYPE[dt], KDA_ALGO[algo])
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
     host = None
     if cu_seqlens_host is not None:
-        if cu_seqlens_host.numel() != N + 1:
-            raise ValueError("cu_seqlens_host must have cu_seqlens' length")
+        if cu_seqlens_host.numel() != N + 1 or cu_seqlens_host.device.type != "cpu":
+            raise ValueError("cu_seqlens_host must be a CPU tensor of cu_seqlens' length")
         ch = cu_seqlens_host.to(torch.int32).contiguous()
         host = ch.data_ptr()
     ws_ptr, ws_bytes = None, 0
@@ -446,15 +441,24 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
         ws_bytes = workspace.numel() * workspace.element_size()
     pool, rows = _pool(state, H, dk, dv, dev)
     cols = block_table.shape[1] if block_table is not None else 0
-    _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream,
-          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, (T, H, dv)),
-          _ptr(g, "g", torch.float32, dev, (T, H)), _ptr(beta, "beta", torch.float32, dev, (T, H)),
-          _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev, (N + 1,)), host, N, T, Hk, H, dk, dv,
-          KDA_DTYPE[dt], scale, pool, rows, _ptr(src_slots, "src_slots", torch.int32, dev, (N,)),
-          _ptr(dst_slots, "dst_slots", torch.int32, dev, (N,)),
-          _ptr(ctx_lens, "ctx_lens", torch.int32, dev, (N,)),
-          _ptr(block_table, "block_table", torch.int32, dev, (N, cols)), cols, block_size,
-          _ptr(o, "o", dt, dev, v.shape), ws_ptr, ws_bytes, KDA_ALGO[algo])
+    args = [_ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, (T, H, dv)),
+            _ptr(g, "g", torch.float32, dev, (T, H)), _ptr(beta, "beta", torch.float32, dev, (T, H)),
+            _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev, (N + 1,)), host, N, T, Hk, H, dk, dv,
+            KDA_DTYPE[dt], scale, pool, rows, _ptr(src_slots, "src_slots", torch.int32, dev, (N,)),
+            _ptr(dst_slots, "dst_slots", torch.int32, dev, (N,)),
+            _ptr(ctx_lens, "ctx_lens", torch.int32, dev, (N,)),
+            _ptr(block_table, "block_table", torch.int32, dev, (N, cols)), cols, block_size,
+            _ptr(o, "o", dt, dev, v.shape), ws_ptr, ws_bytes, KDA_ALGO[algo]]
+    try:
+        _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream, *args)
+    except KdaError as e:
+        if e.code != 3:            # KDA_ERR_WORKSPACE: nothing was launched
+            raise
+        need = kda_gdr_prefill_workspace_size(T, N, Hk, H, dk, dv, dt, algo)
+        with torch.cuda.stream(stream):        # the memory belongs to the stream that uses it
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        args[-3:-1] = workspace.data_ptr(), need
+        _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream, *args)
     return o
 
 

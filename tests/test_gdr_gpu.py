@@ -658,7 +658,7 @@ def test_binding_checks_shapes(K):
            dict(src_slots=i32([0, 1])), dict(dst_slots=i32([0]).long()), dict(ctx_lens=i32([0, 1])),
            dict(q=d["q"].half(), k=d["k"].half()), dict(o=torch.empty_like(d["q"])),
            dict(block_table=i32([[0], [1]]), block_size=64),
-           dict(cu_seqlens_host=torch.tensor([0, 3, 6], dtype=torch.int32))]
+           dict(cu_seqlens_host=torch.tensor([0, 3, 6], dtype=torch.int32)), dict(cu_seqlens_host=cu)]
     for kw in bad:
         with pytest.raises((ValueError, TypeError)):
             K.kda_gdr_prefill(**{**args, **kw})
@@ -743,6 +743,14 @@ def test_prefill_workspace_is_checked(K):
     ws.fill_(0xFF)             # (NaN) nothing is kept there between calls
     b = K.kda_gdr_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, workspace=ws)
     assert torch.equal(a, b)
+    small, other = torch.empty(64, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    c = K.kda_gdr_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, workspace=small)   # replaced
+    assert torch.equal(a, c)
+    c.zero_()
+    torch.cuda.synchronize()
+    K.kda_gdr_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, o=c, stream=other)
+    other.synchronize()
+    assert torch.equal(a, c)
 
 
 @pytest.mark.parametrize("block", [0, 64])
