@@ -798,3 +798,19 @@ def test_prefill_fills_the_device(K):
     state = U.pool(6, H, 128, 128, seed=101)
     for algo in algos_for("bf16", 128, 128):
         check_prefill(K, x, lens, H, state, [0, 1, 2], [3, 4, 5], 0.5, "bf16", algo)
+
+
+def test_empty_batches(K):
+    """No requests, no sequences, no tokens: nothing is read or written past the fixed outputs."""
+    none, head = torch.zeros(0, dtype=torch.int32, device="cuda"), i32([3])
+    p = K.kda_block_plan(none, none, i32([5, 6]), head, torch.zeros(0, 4, dtype=torch.int32, device="cuda"), 16, 5)
+    assert p.cu_seqlens.tolist() == [0] and p.free_head.tolist() == [3]
+    assert p.positions.tolist() == [-1] * 5 and p.token_slots.tolist() == [-1] * 5
+    p = K.kda_block_plan(i32([0, 0]), None, none, i32([0]), i32([[7], [8]]), 16, 0)
+    assert p.cu_seqlens.tolist() == [0, 0, 0] and p.dst_slots.tolist() == [-1, -1]
+    for dt, d in ((torch.bfloat16, 128), (torch.float32, 64)):
+        e, st = dev(U.tokens((0,), 1, 2, d, d, dt, seed=1)), torch.ones(2, 2, d, d, device="cuda")
+        o = K.kda_gdr_decode(e["q"], e["k"], e["v"], e["g"], e["beta"], st)
+        assert o.shape == (0, 2, d)
+        o = K.kda_gdr_prefill(e["q"], e["k"], e["v"], e["g"], e["beta"], i32([0]), state=st)
+        assert o.shape == (0, 2, d) and bool((st == 1.0).all())
