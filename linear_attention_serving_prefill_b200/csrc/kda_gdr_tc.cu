@@ -59,6 +59,7 @@
 
 #include "kda_common.cuh"
 #include "kda_gdr.h"
+#include "kda_gdr_split.h"
 #include "kda_prefill_tc.h"
 #include "tc_ptx.cuh"
 
@@ -143,9 +144,8 @@ struct Item {
     uint8_t part, parts;    // segment, of how many
     Kind kind;
 };
-constexpr int kSms = 148;   // CTAs at once: a split fills them at most once per launch
-constexpr int kMinSplit = 16 * kC, kMaxParts = 64;   // tokens of a call; segments of a sequence
-constexpr int kSplitCost = 3;                        // of the two more launches, in chunks
+constexpr int kSms = kSplitSms;
+static_assert(kSplitChunk == kC, "segments are whole chunks");
 
 struct Params {
     GdrArgs a;
@@ -1216,48 +1216,6 @@ gdr_join_kernel(const __grid_constant__ Joins prm)
     }
 }
 
-// Segments of at most `chunks` chunks, for a sequence of n of them.
-int parts_of(int n, int chunks) { return n > chunks ? (n + chunks - 1) / chunks : 1; }
-bool may_split(const GdrArgs &a) { return (int64_t)a.H * (a.num_seqs + 1) <= kSms && a.total_tokens >= kMinSplit; }
-
-// The segment size (in chunks) of the split that ends first, or 0 where whole sequences do.  Both
-// launches fit the device once.  Without host offsets the lengths are taken as equal.
-int plan_split(const GdrArgs &a)
-{
-    if (!may_split(a)) return 0;
-    int lens[kSms], longest = 0;
-    for (int n = 0; n < a.num_seqs; ++n) {
-        const int64_t L = a.cu_host ? a.cu_host[n + 1] - a.cu_host[n] : (a.total_tokens + a.num_seqs - 1) / a.num_seqs;
-        lens[n] = (int)((L + kC - 1) / kC);
-        longest = lens[n] > longest ? lens[n] : longest;
-    }
-    auto fits = [&](int chunks) {
-        int64_t first = 0, all = 0;
-        for (int n = 0; n < a.num_seqs; ++n) {
-            const int P = parts_of(lens[n], chunks);
-            if (P > kMaxParts) return false;
-            first += P > 1 ? 2 * P - 3 : 0;
-            all += P;
-        }
-        return first * a.H <= kSms && all * a.H <= kSms;
-    };
-    int lo = 1, hi = longest;      // fits(hi): whole sequences
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (fits(mid)) hi = mid; else lo = mid + 1;
-    }
-    // In chunks (3.15 us): both passes, a join per segment, and the two more launches.  32 heads over
-    // one sequence of 4096 tokens: 179 us in 3 segments, 216 us whole; 2 heads over 40000: 254 us in
-    // 38, 1946 us whole; 1 head over 4096: 223 us in 64 segments, 94 us in 11, 214 us whole; 16 heads over 1100: 62
-    // us in 3, 71 us whole.
-    int best = 0, cost = longest;
-    for (int P = parts_of(longest, hi); P > 1; --P) {
-        const int chunks = (longest + P - 1) / P, c = 2 * chunks + P + kSplitCost;
-        if (c < cost) { best = chunks; cost = c; }
-    }
-    return best;
-}
-
 }  // namespace
 
 template <bool SPLIT>
@@ -1273,12 +1231,8 @@ static cudaError_t launch_chunks(int ctas, const CUtensorMap &q, const CUtensorM
 
 size_t gdr_tensor_core_workspace(int32_t total_tokens, int32_t num_seqs, int32_t H)
 {
-    GdrArgs a{};
-    a.total_tokens = total_tokens;
-    a.num_seqs = num_seqs;
-    a.H = H;
     // Of a sequence's 2 P - 2 buffers per head all but one belong to a CTA of the first launch.
-    return may_split(a) ? (size_t)2 * kSms * kD * kD * sizeof(float) : 0;
+    return may_split({num_seqs, total_tokens, H, nullptr}) ? (size_t)2 * kSms * kD * kD * sizeof(float) : 0;
 }
 
 cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream_t stream)
@@ -1297,7 +1251,8 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
     Params p;
     memset(&p, 0, sizeof(p));
     p.a = a;
-    if (const int chunks = plan_split(a)) {
+    const SplitBatch batch = {a.num_seqs, a.total_tokens, a.H, a.cu_host};
+    if (const int chunks = plan_split(batch)) {
         Joins joins;
         memset(&joins, 0, sizeof(joins));
         joins.a = a;
@@ -1305,8 +1260,7 @@ cudaError_t launch_gdr_tensor_core(const GdrArgs &a, void *workspace, cudaStream
         Params first = p;
         int all = 0, firsts = 0, splits = 0, buf = 0;
         for (int n = 0; n < a.num_seqs; ++n) {
-            const int64_t L = a.cu_host ? a.cu_host[n + 1] - a.cu_host[n] : (a.total_tokens + a.num_seqs - 1) / a.num_seqs;
-            const int P = parts_of((int)((L + kC - 1) / kC), chunks);
+            const int P = parts_of(chunks_of(batch, n), chunks);
             Item it = {(uint16_t)n, (uint16_t)buf, 0, (uint8_t)P, kOutputs};
             for (int s = 0; s < P; ++s) {
                 it.part = (uint8_t)s;
