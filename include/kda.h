@@ -412,7 +412,7 @@ kda_status kda_decode_multi(const void *q, const void *k, const void *v, const v
  * can therefore hold -1.  Several sequences may read one row (a shared prefix);
  * a row that one sequence writes must not be read or written by another in the
  * same call (a data race, not detected), but a sequence may write the row that
- * it reads.
+ * it reads, and a row that it writes several times keeps the latest token's state.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -352,6 +352,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int n = SPLIT ? it.seq : prm.ordered ? prm.order[pos] : pos;
     int tbeg = max(a.cu[n], 0), len = max(min(a.cu[n + 1], a.total_tokens) - tbeg, 0);
     // This segment; those behind the sequence's end (the host's lengths may differ) do nothing.
+    const int whole = len;
     int from = 0;
     bool final = true;
     if (SPLIT) {
@@ -1057,6 +1058,8 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // Tokens left in the current block, and its index (no blocks: more than there are).
         int to_block = a.block > 0 ? a.block - (int)(before % a.block) : 0x7fffffff;
         int blk = a.block > 0 ? (int)(before / a.block) : 0;
+        // Columns of the blocks that this call completes end here.
+        const int64_t done = SPLIT && a.block > 0 ? min((before - from + whole) / a.block, (int64_t)a.table_cols) : 0;
         // g and beta of tokens 2 lane, 2 lane + 1 of this chunk, and of the next if this one is full.
         float g[2], be[2], gn[2], bn[2];
         auto fetch = [&](int from, float (&g)[2], float (&be)[2]) {
@@ -1110,6 +1113,16 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 0xffffffffu, (in0 ? __float_as_uint(bad0) : 0u) | (in1 ? __float_as_uint(bad1) : 0u)));
             // The state's two factors multiply it again and again: to the last bit.
             const float factor = (float)exp2((double)(lane == 0 ? first - shift : GC + shift) * 0x1p-32) + bad;
+            // Segments run at once, so a row that the sequence writes again (its last state, a later
+            // block under the same row) is left to the later token.
+            bool again = false;
+            if (SPLIT && it.kind == kOutputs && a.block > 0 && m == to_block && blk < a.table_cols) {
+                const int32_t *rows = a.table + (size_t)n * a.table_cols;
+                const int row = rows[blk];
+                again = a.dst && a.dst[n] == row;
+                for (int64_t j = (int64_t)blk + 1 + lane; j < done; j += 32) again = again || rows[j] == row;
+                again = __any_sync(0xffffffffu, again);
+            }
             if (lane == 1) in.out = factor;
             if (lane == 0) {
                 in.in = factor;
@@ -1119,7 +1132,7 @@ gdr_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 in.row = -1;
                 if (a.block > 0 && (!SPLIT || it.kind == kOutputs) && m == to_block && blk < a.table_cols) {
                     const int row = a.table[(size_t)n * a.table_cols + blk];
-                    if (row >= 0 && row < a.pool_size) in.row = row;
+                    if (row >= 0 && row < a.pool_size && !again) in.row = row;
                 }
             }
             __syncwarp();

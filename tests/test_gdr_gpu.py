@@ -814,3 +814,24 @@ def test_empty_batches(K):
         assert o.shape == (0, 2, d)
         o = K.kda_gdr_prefill(e["q"], e["k"], e["v"], e["g"], e["beta"], i32([0]), state=st)
         assert o.shape == (0, 2, d) and bool((st == 1.0).all())
+
+
+@pytest.mark.parametrize("L,H", [(1100, 2), (4500, 1), (3000, 16)])
+@pytest.mark.parametrize("what", ["one row", "last row", "two in turn"])
+def test_prefill_few_chains_rows_written_again(K, L, H, what):
+    """A sequence whose blocks share rows, or whose last state goes to an earlier block's row: the
+    latest token's state stays, although the segments run at once."""
+    block, ctx = 128, 70
+    cols = (ctx + L) // block + 1
+    x = U.tokens((L,), 1, H, 128, 128, torch.bfloat16, seed=L, rate=(1e-3, 0.5))
+    state = U.pool(6, H, 128, 128, seed=102)
+    table, dst = torch.full((1, cols), 2, dtype=torch.int32), 3
+    if what == "last row":
+        table[0, 1::2], dst = 4, 2
+    elif what == "two in turn":
+        table[0, 1::2] = 4
+        table[0, -1] = 5             # (the block that this call leaves unfinished)
+    for host in (True, False):
+        for _ in range(3):
+            check_prefill(K, x, [L], H, state, [0], [dst], 1.0, "bf16", "tensor_core", ctx=[ctx],
+                          table=table, block=block, host=host)
