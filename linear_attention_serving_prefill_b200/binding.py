@@ -4,7 +4,8 @@ Every function here checks tensor placement and dtype, passes raw device
 pointers and sizes to the C ABI declared in ``include/kda.h``, and raises
 ``KdaError`` on a non-zero status.  All arithmetic runs in the CUDA library;
 there is no fallback: if the library is missing the import of this module
-fails.
+fails.  Outputs and workspaces that a call makes belong to its ``stream``, as
+tensors made under ``torch.cuda.stream(stream)`` do.
 """
 from __future__ import annotations
 
@@ -101,6 +102,16 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw), its memory belonging to ``stream`` (None: the current one).  Kernels on
+    another stream than a tensor's own would write while the allocator's earlier or later
+    tenants of that memory are in use."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _stream_ptr(stream) -> ctypes.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
@@ -140,12 +151,12 @@ def kda_prefill(q, k, v, z, A, beta, cu_seqlens, cu_seqlens_host=None, initial_s
     if dt not in KDA_DTYPE:
         raise ValueError(f"unsupported dtype {dt}")
     if o is None:
-        o = torch.empty(T, H, dv, dtype=dt, device=q.device)
+        o = _made(stream, torch.empty, T, H, dv, dtype=dt, device=q.device)
     if final_state is None and output_final_state:
-        final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=q.device)
+        final_state = _made(stream, torch.empty, N, H, dk, dv, dtype=torch.float32, device=q.device)
     need = kda_prefill_gated_workspace_size(T, N, H, dk, dv, dt, algo, gate)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
     host = None
     if cu_seqlens_host is not None:
         ch = cu_seqlens_host.to(torch.int32).contiguous()
@@ -198,15 +209,16 @@ def kda_prefill_checkpointed(q, k, v, z, A, beta, cu_seqlens, cu_seqlens_host, c
     N = cu_seqlens.shape[0] - 1
     dt = q.dtype
     if o is None:
-        o = torch.empty(T, H, dv, dtype=dt, device=q.device)
+        o = _made(stream, torch.empty, T, H, dv, dtype=dt, device=q.device)
     if final_state is None:
-        final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=q.device)
+        final_state = _made(stream, torch.empty, N, H, dk, dv, dtype=torch.float32, device=q.device)
     count = kda_checkpoint_count(cu_seqlens_host, checkpoint_every)
     if checkpoints is None:
-        checkpoints = torch.empty(max(count, 1), H, dk, dv, dtype=torch.float32, device=q.device)
+        checkpoints = _made(stream, torch.empty, max(count, 1), H, dk, dv, dtype=torch.float32,
+                            device=q.device)
     need = kda_prefill_workspace_size(T, N, H, dk, dv, dt, algo)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
     ch = cu_seqlens_host.to(torch.int32).contiguous()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     code = _lib.kda_prefill_checkpointed(
@@ -237,9 +249,9 @@ def kda_prefill_noalloc(q, k, v, z, A, beta, cu_seqlens, cu_seqlens_host=None,
     if dt not in KDA_DTYPE:
         raise ValueError(f"unsupported dtype {dt}")
     if o is None:
-        o = torch.empty(T, H, dv, dtype=dt, device=q.device)
+        o = _made(stream, torch.empty, T, H, dv, dtype=dt, device=q.device)
     if final_state is None and output_final_state:
-        final_state = torch.empty(N, H, dk, dv, dtype=torch.float32, device=q.device)
+        final_state = _made(stream, torch.empty, N, H, dk, dv, dtype=torch.float32, device=q.device)
     host = None
     if cu_seqlens_host is not None:
         ch = cu_seqlens_host.to(torch.int32).contiguous()
@@ -272,7 +284,7 @@ def kda_decode_step(q, k, v, z, A, beta, state, slots=None, o=None, stream=None,
     dv = v.shape[2]
     dt = q.dtype
     if o is None:
-        o = torch.empty(B, H, dv, dtype=dt, device=q.device)
+        o = _made(stream, torch.empty, B, H, dv, dtype=dt, device=q.device)
     code = _lib.kda_decode_step_gated(
         _dev(q, "q", dt), _dev(k, "k", dt), _dev(v, "v", dt), _dev(z, "z", dt),
         _dev(A, "A", torch.float32), _dev(beta, "beta", torch.float32), B, H, dk, dv,
@@ -295,7 +307,7 @@ def kda_decode_multi(q, k, v, z, A, beta, state, slots=None, num_tokens=None,
     dv = v.shape[3]
     dt = q.dtype
     if o is None and (want_outputs or not update_state):
-        o = torch.empty(B, Tq, H, dv, dtype=dt, device=q.device)
+        o = _made(stream, torch.empty, B, Tq, H, dv, dtype=dt, device=q.device)
     code = _lib.kda_decode_multi(
         _dev(q, "q", dt), _dev(k, "k", dt), _dev(v, "v", dt), _dev(z, "z", dt),
         _dev(A, "A", torch.float32), _dev(beta, "beta", torch.float32), B, Tq, H, dk, dv,
@@ -327,12 +339,12 @@ def kda_prefill_debug(q, k, v, z, A, beta, cu_seqlens, cu_seqlens_host, initial_
     N = cu_seqlens.shape[0] - 1
     dt = q.dtype
     dev = q.device
-    out = {"o": torch.empty(T, H, dv, dtype=dt, device=dev),
-           "final_state": torch.empty(N, H, dk, dv, dtype=torch.float32, device=dev)}
+    out = {"o": _made(stream, torch.empty, T, H, dv, dtype=dt, device=dev),
+           "final_state": _made(stream, torch.empty, N, H, dk, dv, dtype=torch.float32, device=dev)}
     for name, d in (("G", dk), ("W", dk), ("U", dv), ("delta", dv)):
-        out[name] = torch.full((T, H, d), float("nan"), dtype=torch.float32, device=dev)
+        out[name] = _made(stream, torch.full, (T, H, d), float("nan"), dtype=torch.float32, device=dev)
     need = kda_prefill_workspace_size(T, N, H, dk, dv, dt, "tensor_core")
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    ws = _made(stream, torch.empty, max(need, 1), dtype=torch.uint8, device=dev)
     ch = cu_seqlens_host.to(torch.int32).contiguous()
     code = _lib.kda_prefill_debug(
         _dev(q, "q", dt), _dev(k, "k", dt), _dev(v, "v", dt), _dev(z, "z", dt),
@@ -428,7 +440,7 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     N = cu_seqlens.shape[0] - 1
     dt = q.dtype
     if o is None:
-        o = torch.empty_like(v)
+        o = _made(stream, torch.empty_like, v)
     host = None
     if cu_seqlens_host is not None:
         if cu_seqlens_host.numel() != N + 1 or cu_seqlens_host.device.type != "cpu":
@@ -455,8 +467,7 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
         if e.code != 3:            # KDA_ERR_WORKSPACE: nothing was launched
             raise
         need = kda_gdr_prefill_workspace_size(T, N, Hk, H, dk, dv, dt, algo)
-        with torch.cuda.stream(stream):        # the memory belongs to the stream that uses it
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.empty, need, dtype=torch.uint8, device=q.device)
         args[-3:-1] = workspace.data_ptr(), need
         _call(_lib.kda_gdr_prefill, "kda_gdr_prefill", dev, stream, *args)
     return o
@@ -484,7 +495,7 @@ def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_
     dt, f32, i32 = q.dtype, torch.float32, torch.int32
     vshape, gshape, slots = (*lead, H, dv), (*lead, H), (B,)
     if o is None and (want_outputs or not update_state):
-        o = torch.empty_like(v)
+        o = _made(stream, torch.empty_like, v)
     pool, rows = _pool(state, H, dk, dv, dev)
     _call(_lib.kda_gdr_decode, "kda_gdr_decode", dev, stream,
           _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, vshape),
@@ -528,9 +539,9 @@ def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, bloc
     if out is None:
         # One allocation for the int32 outputs, padded so that the positions are 16-byte aligned.
         at = 3 * N + 2 + -(3 * N + 2) % 4
-        flat = torch.empty(at + total_tokens, dtype=i32, device=new_lens.device)
+        flat = _made(stream, torch.empty, at + total_tokens, dtype=i32, device=new_lens.device)
         cu, src, dst, head, _, pos = flat.split_with_sizes((N + 1, N, N, 1, at - 3 * N - 2, total_tokens))
-        slots = torch.empty(total_tokens, dtype=torch.int64, device=new_lens.device)
+        slots = _made(stream, torch.empty, total_tokens, dtype=torch.int64, device=new_lens.device)
         out = BlockPlan(cu, pos, slots, src, dst, head)
         p = flat.data_ptr()
         cu, src, dst, head, pos, slots = (p, p + 4 * (N + 1), p + 4 * (2 * N + 1), p + 4 * (3 * N + 1),

@@ -835,3 +835,54 @@ def test_prefill_few_chains_rows_written_again(K, L, H, what):
         for _ in range(3):
             check_prefill(K, x, [L], H, state, [0], [dst], 1.0, "bf16", "tensor_core", ctx=[ctx],
                           table=table, block=block, host=host)
+
+
+def stream_calls(K):
+    """Every call that makes its own outputs, with the bytes of each output."""
+    x = dev(U.tokens((2000,), 1, 1, 128, 128, torch.bfloat16, seed=103))
+    one = {n: t[:512].view(64, 8, *t.shape[1:]) for n, t in x.items()}
+    pool = torch.zeros(64, 1, 128, 128, device="cuda")
+    cu, lens, A = i32([0, 2000]), i32([1000] * 2), torch.zeros(1, 128, device="cuda")
+    free, head, table = i32(range(100)), i32([0]), i32([[-1] * 40] * 2)
+    z = x["k"]
+    return {
+        "gdr_prefill": lambda s: [K.kda_gdr_prefill(*x.values(), cu, stream=s)],
+        "gdr_decode": lambda s: [K.kda_gdr_decode(*one.values(), pool, stream=s)],
+        "block_plan": lambda s: [t for n, t in K.kda_block_plan(
+            lens, None, free, head, table, 64, 2000, stream=s)._asdict().items() if n in ("positions", "token_slots")],
+        "prefill": lambda s: K.kda_prefill(x["q"], z, x["v"], z, A, x["beta"], cu, stream=s),
+        "prefill_noalloc": lambda s: K.kda_prefill_noalloc(x["q"], z, x["v"], z, A, x["beta"], cu, stream=s),
+        "prefill_checkpointed": lambda s: K.kda_prefill_checkpointed(
+            x["q"], z, x["v"], z, A, x["beta"], cu, torch.tensor([0, 2000]), 512, stream=s),
+        "decode_multi": lambda s: [K.kda_decode_multi(one["q"], one["k"], one["v"], one["k"], A, one["beta"], pool,
+                                                      stream=s)],
+        "decode_step": lambda s: [K.kda_decode_step(x["q"][:64], z[:64], x["v"][:64], z[:64], A, x["beta"][:64], pool,
+                                                    stream=s)],
+    }
+
+
+@pytest.mark.parametrize("name", ["gdr_prefill", "gdr_decode", "block_plan", "prefill", "prefill_noalloc",
+                                  "prefill_checkpointed", "decode_multi", "decode_step"])
+def test_outputs_belong_to_the_stream_that_writes_them(K, name):
+    """A call on another stream whose results are dropped at once: tensors that the current stream
+    makes and fills meanwhile keep their values."""
+    call, s = stream_calls(K)[name], torch.cuda.Stream()
+    want = [t.clone() for t in call(None)]           # (and buffers of these sizes in the current stream's cache)
+    sizes = [t.numel() * t.element_size() for t in want]
+    torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                # about 10 ms, in front of the call's kernels
+    outs = call(s)
+    where = {t.untyped_storage().data_ptr() for t in outs}
+    del outs
+    mine = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    assert not where & {t.untyped_storage().data_ptr() for t in mine}
+    torch.cuda.synchronize()
+    assert all(bool((t == 77).all()) for t in mine)
+    with torch.cuda.stream(s):                       # and the call itself is the same there
+        got = [t.clone() for t in call(s)]
+    torch.cuda.synchronize()
+    if name in ("gdr_prefill", "prefill", "prefill_noalloc", "prefill_checkpointed"):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert K.kda_device_status() == 0
