@@ -45,16 +45,16 @@ __device__ __forceinline__ int32_t clamp_i32(int64_t x) { return (int32_t)(x > 0
 // Tokens t .. t + kRun - 1 (those below total_tokens): request by binary search among
 // lo .. hi for the first (smallest n with cu[n + 1] > t), by walking for the others.
 // Tokens past the last request get -1.
-__device__ __forceinline__ void write_tokens(const BlockPlanArgs &a, BlockSize B, int64_t t0, int lo, int hi,
-                                             bool vec)
+__device__ __forceinline__ void write_tokens(const BlockPlanArgs &a, BlockSize B, int64_t t0, uint32_t lo,
+                                             uint32_t hi, bool vec)
 {
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
+        const uint32_t mid = (lo + hi) >> 1;
         if (a.cu[mid + 1] > t0) hi = mid; else lo = mid + 1;
     }
     int32_t pos[kRun];
     int64_t slot[kRun];
-    int n = lo;
+    int n = (int)lo;
     int64_t end = n < a.num_seqs ? a.cu[n + 1] : 0;
     int64_t shift = n < a.num_seqs ? (int64_t)(a.ctx_lens ? max(a.ctx_lens[n], 0) : 0) - a.cu[n] : 0;
     uint32_t have = 0xffffffffu;      // block whose table entry is in blk
@@ -111,14 +111,15 @@ plan_rows_kernel(BlockPlanArgs a, BlockSize B, bool tokens_too, bool vec)
     int64_t run_tok = 0, run_blk = head;
     if (tid == 0) a.cu[0] = 0;
     auto from_free = [&](int64_t i) { return i < a.num_free ? a.free_blocks[i] : -1; };
-    for (int base = 0; base < a.num_seqs; base += kTile) {
+    // (Unsigned: requests and a tile's table entries may reach 2^31 - 1, and both counters step past their end.)
+    for (uint32_t base = 0; base < (uint32_t)a.num_seqs; base += kTile) {
         int64_t add[kPer], ctx[kPer], have[kPer], want[kPer];
         int64_t tok = 0, blk = 0;             // of this thread's requests
         int32_t wr = 0;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
-            const int n = base + tid * kPer + u;
-            const bool in = n < a.num_seqs;
+            const uint32_t n = base + tid * kPer + u;
+            const bool in = n < (uint32_t)a.num_seqs;
             add[u] = in ? max(a.new_lens[n], 0) : 0;
             ctx[u] = in && a.ctx_lens ? max(a.ctx_lens[n], 0) : 0;
         }
@@ -159,12 +160,13 @@ plan_rows_kernel(BlockPlanArgs a, BlockSize B, bool tokens_too, bool vec)
         int32_t w = before_w + iw - wr;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
-            const int e = tid * kPer + u, n = base + e;
+            const int e = tid * kPer + u;
+            const uint32_t n = base + e;
             t += add[u];
             sFirst[e] = first;
             sHave[e] = clamp_i32(have[u]);
             sPrefix[e] = w;
-            if (n < a.num_seqs) {
+            if (n < (uint32_t)a.num_seqs) {
                 a.cu[n + 1] = clamp_i32(t);
                 const int32_t *row = a.block_table + (size_t)n * a.table_cols;
                 auto block_at = [&](int64_t j) {
@@ -183,13 +185,13 @@ plan_rows_kernel(BlockPlanArgs a, BlockSize B, bool tokens_too, bool vec)
         run_blk += part[1][31];
         __syncthreads();
 #pragma unroll 4
-        for (int e = tid; e < total_w; e += kRowThreads) {
+        for (uint32_t e = tid; e < (uint32_t)total_w; e += kRowThreads) {
             int lo = 0, hi = kTile - 1;       // the request whose entries hold e
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (sPrefix[mid + 1] > e) hi = mid; else lo = mid + 1;
+                if ((uint32_t)sPrefix[mid + 1] > e) hi = mid; else lo = mid + 1;
             }
-            const int32_t i = e - sPrefix[lo];
+            const int32_t i = (int32_t)(e - sPrefix[lo]);
             a.block_table[(size_t)(base + lo) * a.table_cols + sHave[lo] + i] = from_free(sFirst[lo] + i);
         }
         __syncthreads();
@@ -209,12 +211,12 @@ plan_tokens_kernel(BlockPlanArgs a, BlockSize B, bool vec)
     // Requests of the CTA's first and last token; its threads search between them.
     if ((threadIdx.x & 31) == 0 && threadIdx.x < 64) {
         const int64_t t = threadIdx.x == 0 ? t0 : t0 + kCta - 1;
-        int lo = 0, hi = a.num_seqs;
+        uint32_t lo = 0, hi = a.num_seqs;
         while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
+            const uint32_t mid = (lo + hi) >> 1;
             if (a.cu[mid + 1] > t) hi = mid; else lo = mid + 1;
         }
-        range[threadIdx.x >> 5] = lo;
+        range[threadIdx.x >> 5] = (int)lo;
     }
     __syncthreads();
     const int64_t t = t0 + (int64_t)threadIdx.x * kRun;

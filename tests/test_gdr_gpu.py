@@ -886,3 +886,19 @@ def test_outputs_belong_to_the_stream_that_writes_them(K, name):
     if name in ("gdr_prefill", "prefill", "prefill_noalloc", "prefill_checkpointed"):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert K.kda_device_status() == 0
+
+
+def test_plan_largest_table(K):
+    """All 2^31 - 1 entries of a table newly reached in one call: every one is written, and
+    nothing in front of the table or behind it."""
+    cols, guard = 2 ** 31 - 1, 4096
+    buf = torch.full((cols + 2 * guard,), 7, dtype=torch.int32, device="cuda")
+    table = buf[guard:guard + cols].view(1, cols)
+    p = K.kda_block_plan(i32([cols]), None, i32([5, 6, 4]), i32([0]), table, 1, 4)
+    torch.cuda.synchronize()
+    assert p.cu_seqlens.tolist() == [0, cols] and p.free_head.tolist() == [cols]
+    assert p.src_slots.tolist() == [-1] and p.dst_slots.tolist() == [-1]
+    assert p.positions.tolist() == [0, 1, 2, 3] and p.token_slots.tolist() == [5, 6, 4, -1]
+    assert buf[:guard + 3].tolist() == [7] * guard + [5, 6, 4] and bool((buf[guard + cols:] == 7).all())
+    rest = buf[guard + 3:guard + cols]
+    assert int(rest.min()) == -1 and int(rest.max()) == -1
