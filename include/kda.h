@@ -486,12 +486,35 @@ kda_status kda_gdr_prefill(const void *q, const void *k, const void *v, const fl
  *                [0, Tq]), or NULL for all Tq.  Rows of o past it are left as
  *                they were; a sequence with 0 passes its source state through.
  *   o            may be NULL when update_state is 1.
+ * Only the states after the last applied tokens are written.  Where several tokens may
+ * pass the end of a block that is to keep its state (a replay over a prefix cache), use
+ * kda_gdr_decode_blocks.
  */
 kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const float *g,
                           const float *beta, int32_t B, int32_t Tq, int32_t Hk, int32_t H,
                           int32_t dk, int32_t dv, kda_dtype dt, float scale, float *state,
                           int32_t pool_size, const int32_t *src_slots, const int32_t *dst_slots,
                           const int32_t *num_tokens, int32_t update_state, void *o, void *stream);
+
+/*
+ * kda_gdr_decode with update_state = 1 that also writes, as kda_gdr_prefill does, the
+ * state after every block which the applied tokens complete to that block's row.
+ *
+ *   ctx_lens     device int32 [B]: tokens each sequence had before this call (negative
+ *                counts as 0), or NULL for 0.  Only the block boundaries depend on it.
+ *   block_table  device int32 [B, block_table_cols]: row j of sequence b is the pool row of
+ *                its tokens j block_size .. (j + 1) block_size - 1; columns past
+ *                block_table_cols have no row.
+ *   block_size   any positive number.
+ */
+kda_status kda_gdr_decode_blocks(const void *q, const void *k, const void *v, const float *g,
+                                 const float *beta, int32_t B, int32_t Tq, int32_t Hk, int32_t H,
+                                 int32_t dk, int32_t dv, kda_dtype dt, float scale, float *state,
+                                 int32_t pool_size, const int32_t *src_slots,
+                                 const int32_t *dst_slots, const int32_t *num_tokens,
+                                 const int32_t *ctx_lens, const int32_t *block_table,
+                                 int32_t block_table_cols, int32_t block_size, void *o,
+                                 void *stream);
 
 /*
  * Block tables and slot maps of a batch, built on the device from its request
@@ -518,7 +541,9 @@ kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const flo
  *                   the block, -1 where there is no block.
  *   src_slots, dst_slots  out [num_seqs] or NULL: the block of the request's last token
  *                   before and after this call (-1 = none): the rows that
- *                   kda_gdr_prefill, kda_gdr_decode read and write.
+ *                   kda_gdr_prefill, kda_gdr_decode read and write.  (A call of several
+ *                   tokens may complete blocks on its way to dst_slots: kda_gdr_prefill
+ *                   with block_size, kda_gdr_decode_blocks write their rows too.)
  *   free_head_out   out [1]: free_head plus the blocks needed; a value above num_free
  *                   says how many were missing.  May be free_head itself.
  * Sums that pass 2^31 - 1 are written as 2^31 - 1.

@@ -52,6 +52,8 @@ SIGNATURES = {
                         + [_P] * 2 + [_SZ, _I32, _P], _I32),
     "kda_gdr_decode": ([_P] * 5 + [_I32] * 7 + [_F32, _P, _I32] + [_P] * 3 + [_I32] + [_P] * 2,
                        _I32),
+    "kda_gdr_decode_blocks": ([_P] * 5 + [_I32] * 7 + [_F32, _P, _I32] + [_P] * 5 + [_I32] * 2
+                              + [_P] * 2, _I32),
     "kda_block_plan": ([_P] * 2 + [_I32, _P, _I32, _P, _P] + [_I32] * 3 + [_P] * 7, _I32),
 }
 
@@ -475,14 +477,17 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
 
 def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_tokens=None,
                    update_state: bool = True, scale: float = 1.0, o=None,
-                   want_outputs: bool = True, stream=None):
+                   want_outputs: bool = True, stream=None, ctx_lens=None, block_table=None,
+                   block_size: int = 0):
     """Gated delta rule for one or a few tokens of each sequence; returns o (or None).
 
     q, k [B,Hk,dk] or [B,Tq,Hk,dk], v [B,(Tq,)H,dv], g, beta [B,(Tq,)H] fp32, Tq <= 64;
     ``state`` [P,H,dk,dv] fp32 is the pool.  Sequence b reads row src_slots[b] (None: b)
     and, with ``update_state``, writes row dst_slots[b] (None: the row it read) after its
     first num_tokens[b] tokens; rows outside the pool are zeros / not written.
-    ``update_state=False`` is a verify pass.
+    ``update_state=False`` is a verify pass.  With ``block_size`` > 0 the state after every
+    block of ctx_lens[b] + applied tokens that the call completes goes to its row of
+    ``block_table`` [B, blocks] (kda_gdr_decode_blocks).
     """
     dev = _gdr_device(q, k, v)
     if q.dim() == 3:
@@ -497,14 +502,22 @@ def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_
     if o is None and (want_outputs or not update_state):
         o = _made(stream, torch.empty_like, v)
     pool, rows = _pool(state, H, dk, dv, dev)
-    _call(_lib.kda_gdr_decode, "kda_gdr_decode", dev, stream,
-          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, vshape),
-          _ptr(g, "g", f32, dev, gshape), _ptr(beta, "beta", f32, dev, gshape),
-          B, Tq, Hk, H, dk, dv, KDA_DTYPE[dt], scale, pool, rows,
-          _ptr(src_slots, "src_slots", i32, dev, slots),
-          _ptr(dst_slots, "dst_slots", i32, dev, slots),
-          _ptr(num_tokens, "num_tokens", i32, dev, slots), 1 if update_state else 0,
-          _ptr(o, "o", dt, dev, vshape))
+    args = (_ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, vshape),
+            _ptr(g, "g", f32, dev, gshape), _ptr(beta, "beta", f32, dev, gshape),
+            B, Tq, Hk, H, dk, dv, KDA_DTYPE[dt], scale, pool, rows,
+            _ptr(src_slots, "src_slots", i32, dev, slots),
+            _ptr(dst_slots, "dst_slots", i32, dev, slots),
+            _ptr(num_tokens, "num_tokens", i32, dev, slots))
+    out = _ptr(o, "o", dt, dev, vshape)
+    if block_size == 0:
+        _call(_lib.kda_gdr_decode, "kda_gdr_decode", dev, stream, *args, 1 if update_state else 0, out)
+        return o
+    if not update_state:
+        raise ValueError("block_size needs update_state: a verify pass writes no rows")
+    cols = block_table.shape[1] if block_table is not None else 0
+    _call(_lib.kda_gdr_decode_blocks, "kda_gdr_decode_blocks", dev, stream, *args,
+          _ptr(ctx_lens, "ctx_lens", i32, dev, slots),
+          _ptr(block_table, "block_table", i32, dev, (B, cols)), cols, block_size, out)
     return o
 
 

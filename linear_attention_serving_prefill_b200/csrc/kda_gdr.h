@@ -21,12 +21,13 @@ struct GdrArgs {
     int32_t pool_size;
     const int32_t *src, *dst;       // pool rows per sequence, see the C ABI
     void *o;                        // [tokens, H, dv] (decode: nullptr = no outputs)
-    // Prefill: packed sequences, snapshots.
+    // Prefill: packed sequences.
     const int32_t *cu;              // device [num_seqs + 1]; nullptr = decode layout
     const int32_t *cu_host;         // host copy or nullptr (launch order, segments)
+    // Rows of the blocks that the call completes.
     const int32_t *ctx;             // tokens before this call, or nullptr = 0
     const int32_t *table;           // [num_seqs, table_cols] or nullptr
-    int32_t table_cols, block;      // block = 0: no snapshots
+    int32_t table_cols, block;      // block = 0: none
     // Decode: Tq tokens per sequence, of which num_tokens[n] count.
     int32_t Tq;
     const int32_t *num_tokens;

@@ -107,26 +107,37 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
     return status_of(kda::launch_gdr_tensor_core(a, workspace, (cudaStream_t)stream));
 }
 
-extern "C" kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const float *g,
-                                     const float *beta, int32_t B, int32_t Tq, int32_t Hk,
-                                     int32_t H, int32_t dk, int32_t dv, kda_dtype dt, float scale,
-                                     float *state, int32_t pool_size, const int32_t *src_slots,
-                                     const int32_t *dst_slots, const int32_t *num_tokens,
-                                     int32_t update_state, void *o, void *stream)
+namespace {
+
+// Rows of completed blocks: none (kda_gdr_decode), or as the caller names them.
+struct Blocks {
+    const int32_t *ctx, *table;
+    int32_t cols, size;
+};
+
+kda_status decode(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                  int32_t B, int32_t Tq, int32_t Hk, int32_t H, int32_t dk, int32_t dv, kda_dtype dt,
+                  float scale, float *state, int32_t pool_size, const int32_t *src_slots,
+                  const int32_t *dst_slots, const int32_t *num_tokens, int32_t update_state,
+                  const Blocks *blocks, void *o, void *stream)
 {
     if (B < 0 || Tq < 1 || Tq > 64 || pool_size < 0) return KDA_ERR_INVALID_ARG;
     const kda_status st = check_sizes(Hk, H, dk, dv, dt);
     if (st != KDA_OK) return st;
     if (!isfinite(scale) || (update_state != 0 && update_state != 1)) return KDA_ERR_INVALID_ARG;
     if (!update_state && dst_slots) return KDA_ERR_INVALID_ARG;
+    if (blocks && (blocks->size <= 0 || blocks->cols < 0)) return KDA_ERR_INVALID_ARG;
     if (!o && !update_state) return KDA_ERR_INVALID_ARG;   // verify without outputs does nothing
     if (B == 0) return KDA_OK;
     if (!q || !k || !v || !g || !beta || !state) return KDA_ERR_INVALID_ARG;
     if (!src_slots && pool_size < B) return KDA_ERR_INVALID_ARG;
+    if (blocks && (!blocks->table || blocks->cols == 0)) return KDA_ERR_INVALID_ARG;
     for (const void *p : {q, k, v, (const void *)o, (const void *)state})
         if (p && !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     for (const void *p : {(const void *)g, (const void *)beta, (const void *)src_slots,
-                          (const void *)dst_slots, (const void *)num_tokens})
+                          (const void *)dst_slots, (const void *)num_tokens,
+                          (const void *)(blocks ? blocks->ctx : nullptr),
+                          (const void *)(blocks ? blocks->table : nullptr)})
         if (p && !aligned(p, 4)) return KDA_ERR_INVALID_ARG;
     if ((int64_t)B * Tq > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
 
@@ -137,8 +148,37 @@ extern "C" kda_status kda_gdr_decode(const void *q, const void *k, const void *v
     a.scale = scale;
     a.state = state; a.pool_size = pool_size; a.src = src_slots; a.dst = dst_slots;
     a.num_tokens = num_tokens; a.update = update_state != 0; a.o = o;
+    if (blocks) {
+        a.ctx = blocks->ctx; a.table = blocks->table;
+        a.table_cols = blocks->cols; a.block = blocks->size;
+    }
     return status_of(Tq == 1 ? kda::launch_gdr_step(a, (cudaStream_t)stream)
                              : kda::launch_gdr_recurrent(a, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const float *g,
+                                     const float *beta, int32_t B, int32_t Tq, int32_t Hk,
+                                     int32_t H, int32_t dk, int32_t dv, kda_dtype dt, float scale,
+                                     float *state, int32_t pool_size, const int32_t *src_slots,
+                                     const int32_t *dst_slots, const int32_t *num_tokens,
+                                     int32_t update_state, void *o, void *stream)
+{
+    return decode(q, k, v, g, beta, B, Tq, Hk, H, dk, dv, dt, scale, state, pool_size, src_slots,
+                  dst_slots, num_tokens, update_state, nullptr, o, stream);
+}
+
+extern "C" kda_status kda_gdr_decode_blocks(
+    const void *q, const void *k, const void *v, const float *g, const float *beta, int32_t B,
+    int32_t Tq, int32_t Hk, int32_t H, int32_t dk, int32_t dv, kda_dtype dt, float scale,
+    float *state, int32_t pool_size, const int32_t *src_slots, const int32_t *dst_slots,
+    const int32_t *num_tokens, const int32_t *ctx_lens, const int32_t *block_table,
+    int32_t block_table_cols, int32_t block_size, void *o, void *stream)
+{
+    const Blocks blocks = {ctx_lens, block_table, block_table_cols, block_size};
+    return decode(q, k, v, g, beta, B, Tq, Hk, H, dk, dv, dt, scale, state, pool_size, src_slots,
+                  dst_slots, num_tokens, 1, &blocks, o, stream);
 }
 
 extern "C" kda_status kda_block_plan(const int32_t *new_lens, const int32_t *ctx_lens,

@@ -323,8 +323,9 @@ template <int PARTS> __device__ __forceinline__ Item item_at(const GdrArgs &a, u
 // A few tokens of each of many sequences.  A CTA walks over states; while it applies one
 // state's tokens, the next state's columns and tokens are on their way into shared memory
 // (cp.async; a thread fetches what it keeps, so the state needs no barrier), so that loads
-// and steps overlap although a state fills the registers.
-template <int DK, int DV, typename T>
+// and steps overlap although a state fills the registers.  BLOCKS: the state after a block's last
+// token goes to that block's row.
+template <int DK, int DV, typename T, bool BLOCKS>
 __global__ void __launch_bounds__(32 * kWarpsOf<DV>, 16 / kWarpsOf<DV>)
 gdr_few_kernel(GdrArgs a, uint32_t items)
 {
@@ -388,6 +389,9 @@ gdr_few_kernel(GdrArgs a, uint32_t items)
         if (more) next = item_at<kParts>(a, it + gridDim.x);
         Cols S;
         S.run = 1.f;
+        auto position = [&](int t) { return (uint32_t)(a.ctx ? max(a.ctx[x.n], 0) : 0) + t; };
+        uint32_t to_block = 0;     // tokens left in the current block
+        if (BLOCKS) to_block = a.block - position(0) % a.block;
         for (int base = 0; base == 0 || base < x.len; base += kFew) {
             const int m = min(kFew, x.len - base);
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -428,6 +432,14 @@ gdr_few_kernel(GdrArgs a, uint32_t items)
                 if (o && rq == 0)
                     store_pair(o + ((t0 + t) * a.H + x.h) * DV + x.part * kCols + own_col,
                                make_float2(a.scale * y.x, a.scale * y.y));
+                if (BLOCKS) {
+                    if (--to_block == 0) {
+                        const uint32_t blk = position(base + t) / (uint32_t)a.block;
+                        const int row = blk < (uint32_t)a.table_cols ? a.table[(size_t)x.n * a.table_cols + blk] : -1;
+                        if (row >= 0 && row < a.pool_size) S.store(state_at(x, row));
+                        to_block = a.block;
+                    }
+                }
             }
         }
         if (x.dst >= 0) S.store(state_at(x, x.dst));
@@ -448,7 +460,8 @@ cudaError_t launch_typed(const GdrArgs &a, cudaStream_t stream)
         gdr_recurrent_kernel<DK, DV, T><<<(unsigned)items, kThreads, 0, stream>>>(a);
     } else {
         const int64_t resident = (int64_t)kSms * (16 / kWarpsOf<DV>);
-        gdr_few_kernel<DK, DV, T><<<(unsigned)(items < resident ? items : resident), kThreads, 0, stream>>>(a, (uint32_t)items);
+        auto *kernel = a.block > 0 ? gdr_few_kernel<DK, DV, T, true> : gdr_few_kernel<DK, DV, T, false>;
+        kernel<<<(unsigned)(items < resident ? items : resident), kThreads, 0, stream>>>(a, (uint32_t)items);
     }
     return cudaGetLastError();
 }

@@ -19,7 +19,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSms = 148;
 
-template <int DK, int DV, int COLS, typename T>
+// BLOCKS: a token that completes a block leaves the state in that block's row too (as a value of the
+// arguments instead, 534 to 536 instead of 524 us).
+template <int DK, int DV, int COLS, typename T, bool BLOCKS>
 __global__ void __launch_bounds__(kThreads)
 gdr_step_kernel(GdrArgs a)
 {
@@ -37,6 +39,12 @@ gdr_step_kernel(GdrArgs a)
     if (src < 0 || src >= a.pool_size) src = -1;
     if (!a.update || dst < 0 || dst >= a.pool_size) dst = -1;
     const bool live = !a.num_tokens || a.num_tokens[b] > 0;
+    int kept = -1;            // row of the block that this token completes
+    if (BLOCKS && live) {
+        const uint32_t pos = a.ctx ? max(a.ctx[b], 0) : 0, blk = pos / (uint32_t)a.block;
+        if ((pos + 1) % (uint32_t)a.block == 0 && blk < (uint32_t)a.table_cols) kept = a.table[(size_t)b * a.table_cols + blk];
+        if (kept >= a.pool_size || kept == dst) kept = -1;
+    }
     if (!live && (dst < 0 || dst == src)) return;
     const size_t one = (size_t)DK * DV / 4, row = DV / 4;
     float4 *pool = (float4 *)a.state + part * CG + cg;
@@ -106,16 +114,19 @@ gdr_step_kernel(GdrArgs a)
         }
         __syncthreads();
     }
-    if (dst < 0) return;
     const float4 d = live ? sD[cg] : make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 *S = pool + ((size_t)dst * a.H + h) * one;
+    auto store = [&](int slot) {
+        float4 *S = pool + ((size_t)slot * a.H + h) * one;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        const float kc = live ? sK[rg + i * RG] : 0.f;
-        S[(size_t)(rg + i * RG) * row] =
-            make_float4(fmaf(kc, d.x, s[i].x), fmaf(kc, d.y, s[i].y), fmaf(kc, d.z, s[i].z),
-                        fmaf(kc, d.w, s[i].w));
-    }
+        for (int i = 0; i < RPT; ++i) {
+            const float kc = live ? sK[rg + i * RG] : 0.f;
+            S[(size_t)(rg + i * RG) * row] =
+                make_float4(fmaf(kc, d.x, s[i].x), fmaf(kc, d.y, s[i].y), fmaf(kc, d.z, s[i].z),
+                            fmaf(kc, d.w, s[i].w));
+        }
+    };
+    if (dst >= 0) store(dst);
+    if (BLOCKS && kept >= 0) store(kept);
 }
 
 template <int DK, int DV, typename T>
@@ -126,10 +137,12 @@ cudaError_t launch_typed(const GdrArgs &a, cudaStream_t stream)
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     // Few states: 32 columns per CTA.  Device time of 32 / 96 / 160 / 192 / 288 states of
     // 128 x 128, split: 3.2 / 5.9 / 7.2 / 8.3 / 10.6 us; whole: 4.2 / 6.2 / 8.5 / 8.7 / 9.9 us.
+    auto launch = [&](auto *kernel, int64_t ctas) { kernel<<<(unsigned)ctas, kThreads, 0, stream>>>(a); };
     if (DV > 32 && blocks < 3 * kSms / 2)
-        gdr_step_kernel<DK, DV, 32, T><<<(unsigned)(blocks * (DV / 32)), kThreads, 0, stream>>>(a);
+        launch(a.block > 0 ? gdr_step_kernel<DK, DV, 32, T, true> : gdr_step_kernel<DK, DV, 32, T, false>,
+               blocks * (DV / 32));
     else
-        gdr_step_kernel<DK, DV, DV, T><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+        launch(a.block > 0 ? gdr_step_kernel<DK, DV, DV, T, true> : gdr_step_kernel<DK, DV, DV, T, false>, blocks);
     return cudaGetLastError();
 }
 

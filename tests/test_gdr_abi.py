@@ -137,3 +137,24 @@ def test_reference_step_is_the_product_form():
         assert torch.allclose(o[t, 0], 0.5 * (M.T @ q), rtol=0, atol=1e-14)
     assert torch.allclose(S[1, 0], M, rtol=0, atol=1e-14)
     assert torch.equal(S[0], state[0].double())
+
+
+def decode_blocks(**kw):
+    a = dict(q=P, k=P, v=P, g=P, beta=P, B=4, Tq=3, Hk=2, H=4, dk=128, dv=128, dt=BF16, scale=1.0,
+             state=P, rows=4, src=None, dst=None, nt=None, ctx=None, table=P, cols=2, block=64, o=P, stream=None)
+    a.update(kw)
+    return B._lib.kda_gdr_decode_blocks(*a.values())
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [
+    (dict(B=-1), INVALID), (dict(Tq=0), INVALID), (dict(Tq=65), INVALID), (dict(state=None), INVALID),
+    (dict(rows=3), INVALID), (dict(nt=P + 1), INVALID), (dict(ctx=P + 2), INVALID), (dict(table=P + 2), INVALID),
+    (dict(table=None), INVALID), (dict(cols=0), INVALID), (dict(cols=-1), INVALID), (dict(block=0), INVALID),
+    (dict(block=-64), INVALID)], ids=str)
+def test_decode_blocks_refusals(kw, code):
+    assert decode_blocks(**kw) == code
+
+
+def test_decode_blocks_empty():
+    assert decode_blocks(B=0, table=None, cols=0) == OK
+    assert decode_blocks(B=0, block=0) == INVALID

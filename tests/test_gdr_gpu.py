@@ -902,3 +902,153 @@ def test_plan_largest_table(K):
     assert buf[:guard + 3].tolist() == [7] * guard + [5, 6, 4] and bool((buf[guard + cols:] == 7).all())
     rest = buf[guard + 3:guard + cols]
     assert int(rest.min()) == -1 and int(rest.max()) == -1
+
+
+@pytest.mark.parametrize("Tq,block", [(1, 1), (1, 64), (2, 64), (4, 3), (5, 5), (9, 1), (64, 16), (64, 1000)])
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 128, 128), ("f32", 128, 64), ("f32", 32, 32), ("bf16", 64, 128)])
+def test_decode_block_rows(K, Tq, block, dtype, dk, dv):
+    """A few tokens at and across block ends: every completed block's row keeps the state at its
+    end; rows outside the pool, columns past the table and unfinished blocks get none."""
+    B, Hk, H = 7, 2, 4
+    x = U.tokens((B * Tq,), Hk, H, dk, dv, DT[dtype], seed=104 + Tq)
+    nt = [Tq, 0, (Tq + 1) // 2, Tq, Tq, 1, Tq]
+    ctx = [0, 2 * block - 1, block - 1, -5, max(2 * block - 2, 0), 3 * block - 1, 5]
+    pos = [max(c, 0) for c in ctx]
+    cols = max((c + n) // block for c, n in zip(pos, nt)) + 1
+    state = U.pool(2 * B + B * cols + 1, H, dk, dv, seed=105)
+    table = torch.arange(2 * B, 2 * B + B * cols, dtype=torch.int32).view(B, cols)
+    table[3, 0], table[4, -1] = -1, state.shape[0]
+    if cols > 1:
+        table[6] = table[6, 0]                     # every block under one row: the latest state stays
+    src = [0, 1, -1, 3, 4, 5, 6]
+    d = {n: t.cuda().view(B, Tq, *t.shape[1:]) for n, t in x.items()}
+    spans = [(b * Tq, nt[b]) for b in range(B)]
+    in_place = [0, 1, -1, 3, int(table[4, pos[4] // block]), 5, 6]
+    for dst in ([B + b for b in range(B)], in_place, None):
+        for short in (0, 1):
+            tab = table[:, :cols - short].contiguous()
+            if tab.shape[1] == 0:
+                continue
+            ref_o, ref_S = U.reference(x, spans, H, 0.7, state, src, src if dst is None else dst, pos, tab, block)
+            live = torch.isfinite(ref_o)
+            st, o = state.cuda(), torch.full_like(d["v"], 7.0)
+            K.kda_gdr_decode(d["q"], d["k"], d["v"], d["g"], d["beta"], st, src_slots=i32(src), dst_slots=i32(dst),
+                             num_tokens=i32(nt), scale=0.7, o=o, ctx_lens=i32(ctx), block_table=i32(tab),
+                             block_size=block)
+            flat = o.view(B * Tq, H, dv).cpu()
+            assert bool((flat[~live] == 7.0).all())
+            assert U.max_err(flat[live], ref_o[live]) <= TOL_O[dtype]
+            for r in range(state.shape[0]):
+                if torch.equal(ref_S[r], state[r].double()):
+                    assert torch.equal(st[r].cpu(), state[r]), r
+                else:
+                    assert U.max_err(st[r], ref_S[r]) <= TOL_F32, r
+
+
+def test_decode_block_rows_leave_results_alone(K):
+    """The same outputs and last rows, bit by bit, with and without blocks; no context is position 0."""
+    B, Tq, H = 40, 6, 24
+    x = U.tokens((B * Tq,), 6, H, 128, 128, torch.bfloat16, seed=106)
+    d = {n: t.cuda().view(B, Tq, *t.shape[1:]) for n, t in x.items()}
+    state = U.pool(3 * B, H, 128, 128, seed=107)
+    table = torch.arange(B, 3 * B, dtype=torch.int32).view(B, 2)
+    for tq in (1, Tq):
+        y = {n: t[:, :tq].contiguous() for n, t in d.items()}
+        a, b, c = state.cuda(), state.cuda(), state.cuda()
+        oa = K.kda_gdr_decode(*y.values(), a)
+        ob = K.kda_gdr_decode(*y.values(), b, block_table=i32(table), block_size=3)
+        oc = K.kda_gdr_decode(*y.values(), c, ctx_lens=i32([0] * B), block_table=i32(table), block_size=3)
+        assert torch.equal(oa, ob) and torch.equal(a[:B], b[:B]) and torch.equal(b, c)
+        if tq == 1:
+            assert torch.equal(b[B:].cpu(), state[B:])
+        else:                                       # the second block ends with the call
+            assert torch.equal(b[B + 1::2], a[:B]) and not torch.equal(b[B::2].cpu(), state[B::2])
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_verify_and_replay_run_across_block_ends(K, graph):
+    """Plan -> prefill -> (plan of the accepted tokens -> verify of the drafts -> replay) ...: every
+    completed block's row and the last rows equal the plain form."""
+    prompt, steps, Tq, H, block = [62, 128, 1, 191], 20, 4, 2, 64
+    N = len(prompt)
+    gen = torch.Generator().manual_seed(108)
+    acc = torch.randint(0, Tq + 1, (steps, N), generator=gen)
+    acc[0], acc[1] = torch.tensor([4, 1, 4, 0]), torch.tensor([0, 4, 4, 3])
+    total = [prompt[n] + int(acc[:, n].sum()) for n in range(N)]
+    room = [t + Tq for t in total]                   # drafts behind the last accepted token
+    x = U.tokens((sum(room),), 1, H, 128, 128, torch.bfloat16, seed=109)
+    start = U.cu_of(room).tolist()[:N]
+    need = sum(-(-t // block) for t in total)
+    cols = max(-(-t // block) for t in total) + 1
+    ref_table, at = torch.full((N, cols), -1, dtype=torch.int32), 0
+    for n, t in enumerate(total):
+        ref_table[n, :-(-t // block)] = torch.arange(at, at - (-t // block))
+        at += -(-t // block)
+    last = [int(ref_table[n, (t - 1) // block]) for n, t in enumerate(total)]
+    ref_o, ref_S = U.reference(x, list(zip(start, total)), H, 0.5, torch.zeros(need, H, 128, 128), None, last, None,
+                               ref_table, block)
+    d = dev(x)
+    table = torch.full((N, cols), -1, dtype=torch.int32, device="cuda")
+    free, head = torch.randperm(need, generator=gen).to(torch.int32).cuda(), i32([0])
+    pool = torch.full((need, H, 128, 128), float("nan"), device="cuda")
+    new, ctx = i32(prompt), i32([0] * N)
+    p = K.kda_block_plan(new, ctx, free, head, table, block, sum(prompt))
+    idx = torch.cat([torch.arange(start[n], start[n] + prompt[n]) for n in range(N)]).cuda()
+    K.kda_gdr_prefill(*(t[idx].contiguous() for t in d.values()), p.cu_seqlens, state=pool, src_slots=p.src_slots,
+                      dst_slots=p.dst_slots, ctx_lens=ctx, block_table=table, block_size=block, scale=0.5)
+    head.copy_(p.free_head)
+    ctx.copy_(new)
+    tok = {n: torch.empty(N, Tq, *t.shape[1:], dtype=t.dtype, device="cuda") for n, t in d.items()}
+    drafts, plan = torch.empty_like(tok["v"]), p._replace(
+        positions=torch.empty(N * Tq, dtype=torch.int32, device="cuda"),
+        token_slots=torch.empty(N * Tq, dtype=torch.int64, device="cuda"), free_head=head)
+
+    def step():
+        K.kda_block_plan(new, ctx, free, head, table, block, N * Tq, out=plan)
+        K.kda_gdr_decode(*tok.values(), pool, src_slots=plan.src_slots, update_state=False, scale=0.5, o=drafts)
+        K.kda_gdr_decode(*tok.values(), pool, src_slots=plan.src_slots, dst_slots=plan.dst_slots, num_tokens=new,
+                         want_outputs=False, ctx_lens=ctx, block_table=table, block_size=block)
+        ctx.add_(new)
+
+    run = step
+    if graph:
+        keep = [t.clone() for t in (ctx, head, table, pool)]
+        new.zero_()                                  # (the warm-up adds nothing)
+        for t in tok.values():
+            t.zero_()
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        run = g.replay
+        for t, k in zip((ctx, head, table, pool), keep):
+            assert torch.equal(t.nan_to_num(9.0), k.nan_to_num(9.0))
+    for i in range(steps):
+        at = torch.tensor(start).cuda()[:, None] + ctx[:, None] + torch.arange(Tq).cuda()
+        for n, t in d.items():
+            tok[n].copy_(t[at])
+        new.copy_(acc[i])
+        run()
+        for n in range(N):
+            a, b = int(at[n, 0]), int(acc[i, n])
+            if b:
+                assert U.max_err(drafts[n, :b], ref_o[a:a + b]) <= TOL_TC
+    torch.cuda.synchronize()
+    assert ctx.tolist() == total and int(head) == need
+    for n, t in enumerate(total):
+        for j in range(-(-t // block)):
+            assert U.max_err(pool[int(table[n, j])], ref_S[int(ref_table[n, j])]) <= TOL_TC_S, (n, j)
+
+
+def test_decode_blocks_checks(K):
+    d = dev(U.tokens((3,), 1, 2, 64, 64, torch.float32, seed=110))
+    st, args = torch.zeros(3, 2, 64, 64, device="cuda"), list(d.values())
+    ok = dict(block_table=i32([[0]] * 3), block_size=2, ctx_lens=i32([0, 1, 1]))
+    K.kda_gdr_decode(*args, st, **ok)
+    for kw in [dict(update_state=False), dict(block_table=i32([[0]])), dict(block_table=i32([[0]] * 3).long()),
+               dict(ctx_lens=i32([0])), dict(ctx_lens=torch.zeros(3, device="cuda"))]:
+        with pytest.raises(ValueError):
+            K.kda_gdr_decode(*args, st, **{**ok, **kw})
+    for kw in [dict(block_table=None), dict(block_size=-2)]:
+        with pytest.raises(K.KdaError):
+            K.kda_gdr_decode(*args, st, **{**ok, **kw})
