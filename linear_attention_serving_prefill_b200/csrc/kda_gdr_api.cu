@@ -127,8 +127,8 @@ kda_status decode(const void *q, const void *k, const void *v, const float *g, c
     if (!isfinite(scale) || (update_state != 0 && update_state != 1)) return KDA_ERR_INVALID_ARG;
     if (!update_state && dst_slots) return KDA_ERR_INVALID_ARG;
     if (blocks && (blocks->size <= 0 || blocks->cols < 0)) return KDA_ERR_INVALID_ARG;
-    if (!o && !update_state) return KDA_ERR_INVALID_ARG;   // verify without outputs does nothing
     if (B == 0) return KDA_OK;
+    if (!o && !update_state) return KDA_ERR_INVALID_ARG;   // verify without outputs does nothing
     if (!q || !k || !v || !g || !beta || !state) return KDA_ERR_INVALID_ARG;
     if (!src_slots && pool_size < B) return KDA_ERR_INVALID_ARG;
     if (blocks && (!blocks->table || blocks->cols == 0)) return KDA_ERR_INVALID_ARG;

@@ -158,3 +158,10 @@ def test_decode_blocks_refusals(kw, code):
 def test_decode_blocks_empty():
     assert decode_blocks(B=0, table=None, cols=0) == OK
     assert decode_blocks(B=0, block=0) == INVALID
+
+
+def test_empty_verify():
+    """A verify pass of no sequences: its empty output arrives as a null pointer."""
+    assert decode(B=0, update=0, o=None) == OK
+    assert decode(B=0, update=0, o=None, q=None, k=None, v=None, g=None, beta=None) == OK
+    assert decode(B=0, update=0, dst=P) == INVALID and decode(B=0, update=2) == INVALID

@@ -1052,3 +1052,14 @@ def test_decode_blocks_checks(K):
     for kw in [dict(block_table=None), dict(block_size=-2)]:
         with pytest.raises(K.KdaError):
             K.kda_gdr_decode(*args, st, **{**ok, **kw})
+
+
+def test_empty_verify(K):
+    for dt, d in ((torch.bfloat16, 128), (torch.float32, 64)):
+        st = torch.ones(2, 2, d, d, device="cuda")
+        for lead in ((0,), (0, 4)):
+            e = dev(U.tokens(lead, 1, 2, d, d, dt, seed=1))
+            assert K.kda_gdr_decode(*e.values(), st, update_state=False).shape == (*lead, 2, d)
+            table = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+            assert K.kda_gdr_decode(*e.values(), st, block_table=table, block_size=4).shape == (*lead, 2, d)
+        assert bool((st == 1.0).all())
