@@ -70,7 +70,8 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
     if (!isfinite(scale) || pool_size < 0 || block_size < 0 || block_size % 64 != 0 ||
         block_table_cols < 0)
         return KDA_ERR_INVALID_ARG;
-    if (num_seqs > 0 && !cu_seqlens_dev) return KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return KDA_OK;
+    if (!cu_seqlens_dev) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!q || !k || !v || !g || !beta || !o)) return KDA_ERR_INVALID_ARG;
     if (!state && (src_slots || dst_slots || block_size > 0)) return KDA_ERR_INVALID_ARG;
     if (block_size > 0 && (!block_table || block_table_cols == 0)) return KDA_ERR_INVALID_ARG;
@@ -88,7 +89,6 @@ extern "C" kda_status kda_gdr_prefill(const void *q, const void *k, const void *
     }
     const size_t need = kda_gdr_prefill_workspace_size(total_tokens, num_seqs, Hk, H, dk, dv, dt, algo);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
-    if (num_seqs == 0) return KDA_OK;
 
     kda::GdrArgs a{};
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;

@@ -29,7 +29,7 @@ inline int parts_of(int n, int chunks) { return n > chunks ? (n + chunks - 1) / 
 
 inline bool may_split(const SplitBatch &b)
 {
-    return (int64_t)b.H * ((int64_t)b.num_seqs + 1) <= kSplitSms && b.total_tokens >= kMinSplit;
+    return b.num_seqs > 0 && (int64_t)b.H * ((int64_t)b.num_seqs + 1) <= kSplitSms && b.total_tokens >= kMinSplit;
 }
 
 // The segment size (in chunks) of the split that ends first, or 0 where whole sequences do.  Both

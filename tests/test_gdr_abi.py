@@ -165,3 +165,14 @@ def test_empty_verify():
     assert decode(B=0, update=0, o=None) == OK
     assert decode(B=0, update=0, o=None, q=None, k=None, v=None, g=None, beta=None) == OK
     assert decode(B=0, update=0, dst=P) == INVALID and decode(B=0, update=2) == INVALID
+
+
+def test_empty_prefill():
+    """No sequences: nothing is read, whatever the blocks' empty table, the offsets or a
+    padded token count would need otherwise."""
+    assert prefill(N=0, T=0, block=64, table=None, cols=4) == OK
+    assert prefill(N=0, T=0, block=64, table=None, cols=0) == OK
+    assert prefill(N=0, T=5000, Hk=1, H=2) == OK
+    assert B.kda_gdr_prefill_workspace_size(5000, 0, 1, 2, 128, 128) == 0
+    assert prefill(N=0, T=0, block=32) == INVALID and prefill(N=0, T=0, cols=-1) == INVALID
+    assert prefill(N=0, T=-1) == INVALID and prefill(N=0, rows=-1) == INVALID

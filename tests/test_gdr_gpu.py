@@ -1063,3 +1063,13 @@ def test_empty_verify(K):
             table = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
             assert K.kda_gdr_decode(*e.values(), st, block_table=table, block_size=4).shape == (*lead, 2, d)
         assert bool((st == 1.0).all())
+
+
+def test_empty_prefill(K):
+    for dt, d in ((torch.bfloat16, 128), (torch.float32, 64)):
+        st, table = torch.ones(2, 2, d, d, device="cuda"), torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+        for T in (0, 2000):
+            e = dev(U.tokens((T,), 1, 2, d, d, dt, seed=1))
+            o = torch.full_like(e["v"], 7.0)
+            K.kda_gdr_prefill(*e.values(), i32([0]), state=st, block_table=table, block_size=64, o=o)
+            assert bool((o == 7.0).all()) and bool((st == 1.0).all())
