@@ -385,6 +385,12 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype, index: int, shape=None):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _count(n: int, name: str) -> None:
+    """A number that the C interface takes in 32 bits."""
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name} does not fit 32 bits: {n}")
+
+
 def _call(fn, where: str, index: int, stream, *args):
     """One library call on device ``index``, on ``stream`` or that device's current stream."""
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
@@ -436,6 +442,7 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     every completed block of ctx_lens[n] + new tokens goes to its row of ``block_table``
     [N, blocks].
     """
+    _count(block_size, "block_size")
     dev = _gdr_device(q, k, v)
     T, Hk, dk = q.shape
     _, H, dv = v.shape
@@ -489,6 +496,7 @@ def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_
     block of ctx_lens[b] + applied tokens that the call completes goes to its row of
     ``block_table`` [B, blocks] (kda_gdr_decode_blocks).
     """
+    _count(block_size, "block_size")
     dev = _gdr_device(q, k, v)
     if q.dim() == 3:
         B, Hk, dk = q.shape
@@ -541,12 +549,15 @@ def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, bloc
     the token outputs (entries past the last token are -1).  Returns a ``BlockPlan``;
     ``out`` passes its tensors (``out.free_head`` may be ``free_head`` itself).
     """
+    _count(block_size, "block_size")
+    _count(total_tokens, "total_tokens")
     dev = new_lens.get_device()
     if dev < 0:
         raise ValueError("new_lens must be a CUDA tensor")
     (N,), (F,), i32 = new_lens.shape, free_blocks.shape, torch.int32
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must have shape ({N}, blocks)")
+    _count(max(N, F, block_table.shape[1]), "a length of new_lens, free_blocks or block_table")
     if total_tokens < 0:
         raise ValueError("total_tokens must not be negative")
     if out is None:

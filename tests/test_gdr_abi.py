@@ -176,3 +176,19 @@ def test_empty_prefill():
     assert B.kda_gdr_prefill_workspace_size(5000, 0, 1, 2, 128, 128) == 0
     assert prefill(N=0, T=0, block=32) == INVALID and prefill(N=0, T=0, cols=-1) == INVALID
     assert prefill(N=0, T=-1) == INVALID and prefill(N=0, rows=-1) == INVALID
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """The C interface counts in 32 bits; a larger number is refused, not taken modulo 2^32."""
+    x = U.tokens((4,), 1, 2, 32, 32, torch.float32, seed=0)
+    one, table = torch.ones(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    cu, state = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(4, 2, 32, 32)
+    for bad in (1 << 31, (1 << 32) + 64, -(1 << 32) + 64):
+        with pytest.raises(ValueError, match="block_size"):
+            B.kda_gdr_prefill(*x.values(), cu, state=state, block_table=table, block_size=bad)
+        with pytest.raises(ValueError, match="block_size"):
+            B.kda_gdr_decode(*x.values(), state, block_table=table, block_size=bad)
+        with pytest.raises(ValueError, match="block_size"):
+            B.kda_block_plan(one, None, one, one, table, bad, 1)
+        with pytest.raises(ValueError, match="total_tokens"):
+            B.kda_block_plan(one, None, one, one, table, 16, bad)
