@@ -460,8 +460,11 @@ size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, in
  * The tensor-core path holds the state in fp32 and its operands in two bf16 numbers each
  * (state within 2e-5 of the recurrence in 64 bits, 2-norm; o rounded to bf16 after products
  * whose S and P are single bf16 numbers), for keys with beta |k|^2 <= 2 (past it the
- * recurrence itself grows from token to token) and |v| up to 2^20.  A NaN or an infinity in a token reaches its own
- * sequence and head, there from the start of the token's chunk of 64 on at the earliest.
+ * recurrence itself grows from token to token) and v and states of sizes from 2^-20 to 2^20
+ * (smaller ones lose bits in single outputs where a head decays by more than 2^100 in 64
+ * tokens; the recurrence of KDA_ALGO_CUDA_CORE has no such limits).  A NaN or an infinity in a
+ * token reaches its own sequence and head, there from the start of the token's chunk of 64 on
+ * at the earliest.
  */
 kda_status kda_gdr_prefill(const void *q, const void *k, const void *v, const float *g,
                            const float *beta, const int32_t *cu_seqlens_dev,

@@ -13,12 +13,14 @@
 //   o_r = scale e^{G_r} (Q S + P F)_r,  S <- e^{G_C} (S + K^T F),
 // so one factor per token remains in R, one at the outputs and one at the state, and K and Q
 // enter the products as their TMA tiles.  e^{-G} has to stay in the floating-point range: a
-// chunk ends early, before the token at which e^{-G} would pass 2^208; up to 2^100 nothing is
-// shifted, between them the chunk's scale is shifted down so that e^{-G} <= 2^100.  What its first
-// tokens read and write of the order of 2^-18 and less then loses bits to bf16's exponents (2^-25
-// is lost; the chunk multiplies the state by less than 2^-100).  With 2^200 as the limit 32768
-// tokens x 96 heads of rates e^-5 .. e took 1.66 instead of 1.62 ms; with 2^220 values of 10^-3 were
-// spoilt.  Relative accuracy is that of the decayed form otherwise: each term is scaled by a
+// chunk ends early, before the token at which e^{-G} would pass 2^192; up to 2^100 nothing is
+// shifted, between them the chunk's scale is shifted down so that e^{-G} <= 2^100 (which leaves room
+// for |v| up to 2^20).  What its first tokens read and write is then up to 2^-92 of its size and has
+// 2^-34 of bf16's exponents left: values from 2^-20 on keep their bits behind steep decays and small
+// betas too.  With a limit of 200 (208), v and S of the order of 2^-18 came out off by a third of
+// their size (by 19 times) in single output rows.  32768 tokens x 96 heads of rates e^-5 .. e: 1.74 ms
+// (200: 1.67, 208: 1.62, 184: 1.84, 168: 2.05, 100: 3.5).
+// Relative accuracy is that of the decayed form otherwise: each term is scaled by a
 // power it keeps to its use.
 //
 // Precision.  K and Q are exact operands.  The others on the state's path, S, R, T and F, are
@@ -74,7 +76,7 @@ constexpr int kD = 128, kC = 64;              // head size, chunk
 // take microseconds.
 constexpr uint32_t kTries = 1u << 20, kSuspendNs = 2000;
 constexpr uint64_t kDrainNs = 2000000000ull;   // limit of the waits at the end of a role
-constexpr int64_t kRange = 208ll << 32, kSafe = 100ll << 32;   // log2 bounds of e^{-G}, fixed point
+constexpr int64_t kRange = 192ll << 32, kSafe = 100ll << 32;   // log2 bounds of e^{-G}, fixed point
 
 constexpr int kChainThreads = 512, kGroupThreads = 128, kAuxThreads = 128;
 constexpr int kIntraWarp = 16, kAuxWarp = 24, kIssueWarp = 28, kLoadWarp = 29, kLoad2Warp = 30, kInfoWarp = 31;

@@ -1073,3 +1073,37 @@ def test_empty_prefill(K):
             o = torch.full_like(e["v"], 7.0)
             K.kda_gdr_prefill(*e.values(), i32([0]), state=st, block_table=table, block_size=64, o=o)
             assert bool((o == 7.0).all()) and bool((st == 1.0).all())
+
+
+@pytest.mark.parametrize("e", [-20, -16, 0, 20])
+@pytest.mark.parametrize("what", ["few bits", "many bits", "single steep tokens", "rates", "rates, small betas"])
+def test_prefill_small_and_large_values(K, e, what):
+    """The rule is linear in v and S: with both scaled by 2^e every output row and every head's
+    state stay within the same roundings, relative to their own size, in heads of every decay."""
+    T, H = 200, 32
+    x = U.tokens((T,), H, H, 128, 128, torch.bfloat16, seed=111)
+    lo, hi = (4.0, 256.0) if what == "few bits" else (90.0, 400.0)
+    x["g"] = (-torch.linspace(lo, hi, H) / 64 * 0.6931472).expand(T, H).contiguous()
+    if what == "single steep tokens":
+        x["g"] = torch.full((T, H), -0.01)
+        x["g"][9::37] = -torch.linspace(1.0, 140.0, H)
+    elif what.startswith("rates"):
+        gen = torch.Generator().manual_seed(113)
+        rate = torch.exp(torch.rand(H, generator=gen) * 3 - 0.5)
+        x["g"] = -rate * torch.nn.functional.softplus(torch.randn(T, H, generator=gen))
+        if "betas" in what:
+            x["beta"] = torch.sigmoid(3 * torch.randn(T, H, generator=gen) - 2)
+    x["v"] = (x["v"].float() * 2.0 ** e).bfloat16()
+    state = U.pool(1, H, 128, 128, seed=112, std=1.0) * 2.0 ** e
+    f = {n: t.double() for n, t in x.items()}
+    S = state[0].double()
+    ref, size = torch.empty(T, H, 128, dtype=torch.float64), torch.empty(T, H, dtype=torch.float64)
+    for t in range(T):
+        S, ref[t] = U.step(S, f["q"][t], f["k"][t], f["v"][t], f["g"][t], f["beta"][t], 1.0)
+        size[t] = S.flatten(1).norm(dim=1)
+    for algo in algos_for("bf16", 128, 128):
+        o, st = run_prefill(K, x, [T], state, [0], [0], algo, 1.0)
+        off = (o.double().cpu() - ref).norm(dim=-1)
+        assert bool((off <= 2.0 ** -8 * (ref.norm(dim=-1) + 2 * size) + TOL_F32 * size).all())
+        off = (st[0].double().cpu() - S).flatten(1).norm(dim=1)
+        assert bool((off <= TOL_TC_S * size[-1]).all())
