@@ -457,14 +457,20 @@ size_t kda_gdr_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, in
  *                   fp32 recurrence on CUDA cores), KDA_ALGO_CUDA_CORE or
  *                   KDA_ALGO_TENSOR_CORE (KDA_ERR_UNSUPPORTED for other types or
  *                   sizes); KDA_ALGO_TENSOR_CORE_SPLIT is KDA_ERR_UNSUPPORTED.
- * The tensor-core path holds the state in fp32 and its operands in two bf16 numbers each
- * (state within 2e-5 of the recurrence in 64 bits, 2-norm; o rounded to bf16 after products
- * whose S and P are single bf16 numbers), for keys with beta |k|^2 <= 2 (past it the
- * recurrence itself grows from token to token) and v and states of sizes from 2^-20 to 2^20
- * (smaller ones lose bits in single outputs where a head decays by more than 2^100 in 64
- * tokens; the recurrence of KDA_ALGO_CUDA_CORE has no such limits).  A NaN or an infinity in a
- * token reaches its own sequence and head, there from the start of the token's chunk of 64 on
- * at the earliest.
+ * The tensor-core path holds the state in fp32 and its operands in two bf16 numbers each;
+ * o is rounded to bf16 after products whose S and P are single bf16 numbers.  Against the
+ * recurrence in 64 bits (2-norm), for beta |k|^2 <= 1:
+ *     keys of a head with a cosine of up to 0.5     state 2e-5, o 3e-3 (1e-2 for q along them)
+ *     nearer or equal keys                          state 5e-5, o 1e-2
+ * beta |k|^2 up to 2 (past it the recurrence itself grows from token to token): the same up to
+ * a cosine of 0.5; the edits of one repeated key alternate in sign there, and their sums leave
+ * up to 5e-3 in the state and 5e-2 in o.  This holds where the norms of a head's keys lie
+ * within a factor of 2^8 of one another in any 64 tokens (2^14: state 1e-3; past that, entries
+ * leave fp16 and become infinite), and for v and states of sizes from 2^-20 to 2^20 (smaller
+ * ones lose bits in single outputs where a head decays by more than 2^100 in 64 tokens).  The
+ * recurrence of KDA_ALGO_CUDA_CORE has none of these limits.  A NaN or an infinity in a token
+ * reaches its own sequence and head, there from the start of the token's chunk of 64 on at the
+ * earliest.
  */
 kda_status kda_gdr_prefill(const void *q, const void *k, const void *v, const float *g,
                            const float *beta, const int32_t *cu_seqlens_dev,

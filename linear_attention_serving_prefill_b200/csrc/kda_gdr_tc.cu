@@ -259,7 +259,10 @@ template <bool TRANS> __device__ __forceinline__ void ldmatrix4(uint32_t saddr, 
 // Off-diagonal block of the inverse of a lower-triangular matrix, transposed: Z^T = (T_jj^T
 // A_ij^T) T_ii^T (the caller negates), W x W blocks with leading dimension kLdT, T's stored
 // transposed, every matrix in two fp16 parts (22 bits) kMLow bytes apart, of whose products
-// all but low x low are taken.  For unit keys and beta <= 1 every entry of T is at most 1.
+// all but low x low are taken.  Where beta |k|^2 <= b, an entry of A, of T or of a product between
+// them is at most b |k_s| / |k_r|: 1 for unit keys and beta <= 1, inside fp16 for norms within 2^14 of
+// one another.  The smallest low part is 2^-24, which the ratio of the norms multiplies in the state:
+// 1.2e-5 at 2^8, 4e-5 at 2^10, 5e-4 at 2^14.
 // This warp forms rows j0 .. j0 + 15 (columns of the block) and, of them, columns
 // i0 .. i0 + 15 (rows of the block).
 template <int W>

@@ -1107,3 +1107,56 @@ def test_prefill_small_and_large_values(K, e, what):
         assert bool((off <= 2.0 ** -8 * (ref.norm(dim=-1) + 2 * size) + TOL_F32 * size).all())
         off = (st[0].double().cpu() - S).flatten(1).norm(dim=1)
         assert bool((off <= TOL_TC_S * size[-1]).all())
+
+
+def keys_around(T, H, cosine, gen):
+    """Unit keys of pairwise cosine ``cosine``: a common direction per head and independent rest."""
+    m = U.unit(torch.randn(1, H, 128, generator=gen))
+    r = torch.randn(T, H, 128, generator=gen)
+    r = U.unit(r - (r * m).sum(-1, keepdim=True) * m)
+    return cosine ** 0.5 * m + (1 - cosine) ** 0.5 * r
+
+
+# (cosine, bound of beta |k|^2, log2 of the span of the norms, log2 of v's size, q along the keys,
+#  state and output errors that the header states)
+STATED = [(0.0, 1.0, 0, 0, False, 2e-5, 3e-3), (0.0, 2.0, 0, 0, False, 2e-5, 3e-3),
+          (0.5, 1.0, 0, 0, False, 2e-5, 3e-3), (0.5, 2.0, 0, 0, False, 2e-5, 3e-3),
+          (0.5, 1.0, 0, 0, True, 2e-5, 1e-2), (0.5, 2.0, 0, 0, True, 2e-5, 1e-2),
+          (0.9, 1.0, 0, 0, False, 5e-5, 1e-2), (0.9, 1.0, 0, 0, True, 5e-5, 1e-2),
+          (0.99, 1.0, 0, 0, True, 5e-5, 1e-2), (1.0, 1.0, 0, 0, False, 5e-5, 1e-2),
+          (0.0, 1.0, 8, 0, False, 2e-5, 3e-3), (0.0, 2.0, 8, 0, False, 2e-5, 3e-3),
+          (0.0, 2.0, 14, 0, False, 1e-3, 3e-3), (0.0, 1.0, 0, 20, False, 2e-5, 3e-3),
+          (0.0, 2.0, 8, -20, False, 2e-5, 3e-3), (1.0, 2.0, 0, 0, False, 5e-3, 5e-2),
+          (1.0, 2.0, 8, 20, False, 5e-3, 5e-2)]
+
+
+@pytest.mark.parametrize("cosine,bound,span,size,along,state_tol,o_tol", STATED)
+@pytest.mark.parametrize("rate", [(1e-4, 1e-3), (1e-3, 0.5), (0.5, 3.0)], ids=["none", "slow", "fast"])
+def test_prefill_stated_accuracy(K, cosine, bound, span, size, along, state_tol, o_tol, rate):
+    """What the header says of the tensor-core path's errors, in 2-norm by head, at the edges of the
+    ranges that it names; and every output row within 2^-8 of what it reads for cosines up to 0.9."""
+    T, H = 400, 4
+    gen = torch.Generator().manual_seed(114)
+    x = U.tokens((T,), H, H, 128, 128, torch.bfloat16, seed=115, rate=rate)
+    k = keys_around(T, H, cosine, gen)
+    x["k"] = (k * 2.0 ** (span * (torch.rand(T, H, 1, generator=gen) - 0.5))).bfloat16()
+    if along:
+        x["q"] = k.bfloat16()
+    u = torch.full((T, H), 0.99) if cosine == 1.0 and bound == 2.0 else torch.rand(T, H, generator=gen)
+    x["beta"] = bound * u / x["k"].float().square().sum(-1)
+    x["v"] = (x["v"].float() * 2.0 ** size).bfloat16()
+    if size == 20:
+        x["v"] = x["v"].clamp(-2.0 ** 20, 2.0 ** 20)
+    state = U.pool(1, H, 128, 128, seed=116, std=1.0) * 2.0 ** size
+    f = {n: t.double() for n, t in x.items()}
+    S = state[0].double()
+    ref, norm = torch.empty(T, H, 128, dtype=torch.float64), torch.empty(T, H, dtype=torch.float64)
+    for t in range(T):
+        S, ref[t] = U.step(S, f["q"][t], f["k"][t], f["v"][t], f["g"][t], f["beta"][t], 1.0)
+        norm[t] = S.flatten(1).norm(dim=1)
+    o, st = run_prefill(K, x, [T], state, [0], [0], "tensor_core", 1.0)
+    off = o.double().cpu() - ref
+    assert bool(((st[0].double().cpu() - S).flatten(1).norm(dim=1) <= state_tol * S.flatten(1).norm(dim=1)).all())
+    assert bool((off.norm(dim=(0, 2)) <= o_tol * ref.norm(dim=(0, 2))).all())
+    if cosine <= 0.9:
+        assert bool((off.norm(dim=-1) <= 2.0 ** -8 * (ref.norm(dim=-1) + 2 * norm)).all())
