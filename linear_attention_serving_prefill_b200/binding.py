@@ -386,7 +386,8 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype, index: int, shape=None):
 
 
 def _count(n: int, name: str) -> None:
-    """A number that the C interface takes in 32 bits."""
+    """A number that the C interface takes in 32 bits (it refuses negative ones itself).  The
+    callers look at n >> 31 first: a call more cost the shortest operators a tenth of a microsecond."""
     if not -0x80000000 <= n <= 0x7fffffff:
         raise ValueError(f"{name} does not fit 32 bits: {n}")
 
@@ -442,7 +443,8 @@ def kda_gdr_prefill(q, k, v, g, beta, cu_seqlens, cu_seqlens_host=None, state=No
     every completed block of ctx_lens[n] + new tokens goes to its row of ``block_table``
     [N, blocks].
     """
-    _count(block_size, "block_size")
+    if block_size >> 31:
+        _count(block_size, "block_size")
     dev = _gdr_device(q, k, v)
     T, Hk, dk = q.shape
     _, H, dv = v.shape
@@ -496,7 +498,8 @@ def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_
     block of ctx_lens[b] + applied tokens that the call completes goes to its row of
     ``block_table`` [B, blocks] (kda_gdr_decode_blocks).
     """
-    _count(block_size, "block_size")
+    if block_size >> 31:
+        _count(block_size, "block_size")
     dev = _gdr_device(q, k, v)
     if q.dim() == 3:
         B, Hk, dk = q.shape
@@ -510,22 +513,22 @@ def kda_gdr_decode(q, k, v, g, beta, state, src_slots=None, dst_slots=None, num_
     if o is None and (want_outputs or not update_state):
         o = _made(stream, torch.empty_like, v)
     pool, rows = _pool(state, H, dk, dv, dev)
-    args = (_ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, vshape),
-            _ptr(g, "g", f32, dev, gshape), _ptr(beta, "beta", f32, dev, gshape),
-            B, Tq, Hk, H, dk, dv, KDA_DTYPE[dt], scale, pool, rows,
-            _ptr(src_slots, "src_slots", i32, dev, slots),
-            _ptr(dst_slots, "dst_slots", i32, dev, slots),
-            _ptr(num_tokens, "num_tokens", i32, dev, slots))
-    out = _ptr(o, "o", dt, dev, vshape)
     if block_size == 0:
-        _call(_lib.kda_gdr_decode, "kda_gdr_decode", dev, stream, *args, 1 if update_state else 0, out)
-        return o
-    if not update_state:
+        fn, where, more = _lib.kda_gdr_decode, "kda_gdr_decode", (1 if update_state else 0,)
+    elif update_state:
+        fn, where = _lib.kda_gdr_decode_blocks, "kda_gdr_decode_blocks"
+        cols = block_table.shape[1] if block_table is not None else 0
+        more = (_ptr(ctx_lens, "ctx_lens", i32, dev, slots),
+                _ptr(block_table, "block_table", i32, dev, (B, cols)), cols, block_size)
+    else:
         raise ValueError("block_size needs update_state: a verify pass writes no rows")
-    cols = block_table.shape[1] if block_table is not None else 0
-    _call(_lib.kda_gdr_decode_blocks, "kda_gdr_decode_blocks", dev, stream, *args,
-          _ptr(ctx_lens, "ctx_lens", i32, dev, slots),
-          _ptr(block_table, "block_table", i32, dev, (B, cols)), cols, block_size, out)
+    _call(fn, where, dev, stream,
+          _ptr(q, "q", dt, dev), _ptr(k, "k", dt, dev), _ptr(v, "v", dt, dev, vshape),
+          _ptr(g, "g", f32, dev, gshape), _ptr(beta, "beta", f32, dev, gshape),
+          B, Tq, Hk, H, dk, dv, KDA_DTYPE[dt], scale, pool, rows,
+          _ptr(src_slots, "src_slots", i32, dev, slots),
+          _ptr(dst_slots, "dst_slots", i32, dev, slots),
+          _ptr(num_tokens, "num_tokens", i32, dev, slots), *more, _ptr(o, "o", dt, dev, vshape))
     return o
 
 
@@ -549,23 +552,31 @@ def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, bloc
     the token outputs (entries past the last token are -1).  Returns a ``BlockPlan``;
     ``out`` passes its tensors (``out.free_head`` may be ``free_head`` itself).
     """
-    _count(block_size, "block_size")
-    _count(total_tokens, "total_tokens")
+    if (block_size | total_tokens) >> 31:
+        _count(block_size, "block_size")
+        _count(total_tokens, "total_tokens")
     dev = new_lens.get_device()
     if dev < 0:
         raise ValueError("new_lens must be a CUDA tensor")
     (N,), (F,), i32 = new_lens.shape, free_blocks.shape, torch.int32
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must have shape ({N}, blocks)")
-    _count(max(N, F, block_table.shape[1]), "a length of new_lens, free_blocks or block_table")
+    M = block_table.shape[1]
+    if (N | F | M) >> 31:
+        _count(max(N, F, M), "a length of new_lens, free_blocks or block_table")
     if total_tokens < 0:
         raise ValueError("total_tokens must not be negative")
     if out is None:
         # One allocation for the int32 outputs, padded so that the positions are 16-byte aligned.
         at = 3 * N + 2 + -(3 * N + 2) % 4
-        flat = _made(stream, torch.empty, at + total_tokens, dtype=i32, device=new_lens.device)
+        device = new_lens.device
+        if stream is None:
+            flat = torch.empty(at + total_tokens, dtype=i32, device=device)
+            slots = torch.empty(total_tokens, dtype=torch.int64, device=device)
+        else:
+            flat = _made(stream, torch.empty, at + total_tokens, dtype=i32, device=device)
+            slots = _made(stream, torch.empty, total_tokens, dtype=torch.int64, device=device)
         cu, src, dst, head, _, pos = flat.split_with_sizes((N + 1, N, N, 1, at - 3 * N - 2, total_tokens))
-        slots = _made(stream, torch.empty, total_tokens, dtype=torch.int64, device=new_lens.device)
         out = BlockPlan(cu, pos, slots, src, dst, head)
         p = flat.data_ptr()
         cu, src, dst, head, pos, slots = (p, p + 4 * (N + 1), p + 4 * (2 * N + 1), p + 4 * (3 * N + 1),
@@ -581,6 +592,6 @@ def kda_block_plan(new_lens, ctx_lens, free_blocks, free_head, block_table, bloc
           _ptr(new_lens, "new_lens", i32, dev, (N,)), _ptr(ctx_lens, "ctx_lens", i32, dev, (N,)),
           N, _ptr(free_blocks, "free_blocks", i32, dev, (F,)), F,
           _ptr(free_head, "free_head", i32, dev, (1,)),
-          _ptr(block_table, "block_table", i32, dev), block_table.shape[1], block_size,
+          _ptr(block_table, "block_table", i32, dev), M, block_size,
           total_tokens, cu, pos, slots, src, dst, head)
     return out
