@@ -967,7 +967,7 @@ def test_decode_block_rows_leave_results_alone(K):
 
 @pytest.mark.parametrize("graph", [False, True])
 def test_verify_and_replay_run_across_block_ends(K, graph):
-    """Plan -> prefill -> (plan of the accepted tokens -> verify of the drafts -> replay) ...: every
+    """Plan -> prefill -> (verify of the drafts -> plan of the accepted ones -> replay) ...: every
     completed block's row and the last rows equal the plain form."""
     prompt, steps, Tq, H, block = [62, 128, 1, 191], 20, 4, 2, 64
     N = len(prompt)
@@ -1004,8 +1004,8 @@ def test_verify_and_replay_run_across_block_ends(K, graph):
         token_slots=torch.empty(N * Tq, dtype=torch.int64, device="cuda"), free_head=head)
 
     def step():
+        K.kda_gdr_decode(*tok.values(), pool, src_slots=plan.dst_slots, update_state=False, scale=0.5, o=drafts)
         K.kda_block_plan(new, ctx, free, head, table, block, N * Tq, out=plan)
-        K.kda_gdr_decode(*tok.values(), pool, src_slots=plan.src_slots, update_state=False, scale=0.5, o=drafts)
         K.kda_gdr_decode(*tok.values(), pool, src_slots=plan.src_slots, dst_slots=plan.dst_slots, num_tokens=new,
                          want_outputs=False, ctx_lens=ctx, block_table=table, block_size=block)
         ctx.add_(new)
