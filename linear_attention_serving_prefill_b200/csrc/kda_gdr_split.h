@@ -57,10 +57,10 @@ inline int plan_split(const SplitBatch &b)
         const int mid = (lo + hi) / 2;
         if (fits(mid)) hi = mid; else lo = mid + 1;
     }
-    // In chunks (3.15 us): both passes, a join per segment, and the two more launches.  32 heads over
-    // one sequence of 4096 tokens: 179 us in 3 segments, 216 us whole; 2 heads over 40000: 254 us in
-    // 38, 1946 us whole; 1 head over 4096: 223 us in 64 segments, 94 us in 11, 214 us whole; 16 heads over 1100: 62
-    // us in 3, 71 us whole.
+    // In chunks (3.15 us): both passes, a join per segment, and the two more launches.  Slow decays:
+    // 32 heads over one sequence of 4096 tokens: 175 us in 3 segments, 216 us whole; 2 heads over
+    // 40000: 251 us in 38, 1946 us whole; 1 head over 4096: 223 us in 64 segments, 87 us in 11, 214 us
+    // whole; 16 heads over 1100: 58 us in 3, 71 us whole.
     int best = 0, cost = longest;
     for (int P = parts_of(longest, hi); P > 1; --P) {
         // (Not below hi: the longest sequence's even division may cut others into more than fits.)

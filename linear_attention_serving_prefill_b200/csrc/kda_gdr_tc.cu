@@ -18,7 +18,7 @@
 // for |v| up to 2^20).  What its first tokens read and write is then up to 2^-92 of its size and has
 // 2^-34 of bf16's exponents left: values from 2^-20 on keep their bits behind steep decays and small
 // betas too.  With a limit of 200 (208), v and S of the order of 2^-18 came out off by a third of
-// their size (by 19 times) in single output rows.  32768 tokens x 96 heads of rates e^-5 .. e: 1.74 ms
+// their size (by 19 times) in single output rows.  32768 tokens x 96 heads of rates e^-5 .. e: 1.75 ms
 // (200: 1.67, 208: 1.62, 184: 1.84, 168: 2.05, 100: 3.5).
 // Relative accuracy is that of the decayed form otherwise: each term is scaled by a
 // power it keeps to its use.
@@ -45,7 +45,7 @@
 //   info  (warp 31)      chunk bounds and factors (a warp scan).
 // K and Q are loaded twice (the second time from L2): A and P are formed up to three chunks
 // ahead of the state, and a tile that stayed for both uses would sit idle in between.
-// One chain takes 3.05 us a chunk alone and 3.1 us at 96 CTAs (32768 tokens x 96 heads: 1.60 ms):
+// One chain takes 3.05 us a chunk alone and 3.1 us at 96 CTAs (32768 tokens x 96 heads of slow decay: 1.58 ms):
 // the state's way through three products and three passes of the chain warps, about 6000 cycles,
 // next to the other roles, which take as long (A and P wait for one accumulator).  Tried and
 // slower: fewer, wider chain warps; register splits between roles; deeper tile rings in place of
